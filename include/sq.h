@@ -53,8 +53,10 @@ typedef enum sq_status {
                                 or size */
     SQ_ERR_CUDA = 3,         /* a CUDA runtime call failed; see sq_last_error_string() */
     SQ_ERR_TIMEOUT = 4,      /* a kernel's bounded wait ran out (reported by sq_get_status) */
-    SQ_ERR_BOUNDS = 5        /* debug builds only (-DSQ_DEBUG): a kernel's index check found a store
-                                outside its buffer and skipped it (reported by sq_get_status) */
+    SQ_ERR_BOUNDS = 5        /* reported by sq_get_status: a page number, length or position that a key/value
+                                cache or prompt call read on the device lies outside its range and was skipped;
+                                in debug builds (-DSQ_DEBUG) also a kernel's index check that found a store
+                                outside its buffer and skipped it */
 } sq_status;
 
 typedef enum sq_dtype {
@@ -422,6 +424,164 @@ sq_status sq_linear_workspace_offsets(int64_t M, int64_t N, int64_t K, sq_dtype 
 sq_status sq_linear(const void* x, const void* w, sq_dtype in_dt, int64_t M, int64_t N,
                     int64_t K, float alpha, float eps, void* y, sq_dtype out_dt,
                     void* workspace, size_t ws_bytes, sq_stream_t stream);
+
+/* ---------------------------------------------------------------- rotary positions
+ * What stands between the QKV projection and the output projection of the same
+ * transformer layer: rotation, a paged 8-bit key/value cache and attention.
+ *
+ * sq_rope_table: the rotation's cosines and sines for positions first_pos ..
+ * first_pos + n_pos - 1,
+ *   f_i        = theta^(-2 i / rot_dim),  i = 0 .. rot_dim/2 - 1
+ *   table[p,i] = magnitude * (cos((first_pos + p) f'_i), sin((first_pos + p) f'_i))
+ * evaluated in fp64 and rounded once. f' is f scaled for contexts longer than
+ * the model was trained on:
+ *   scaling NULL                       f'_i = f_i, magnitude 1
+ *   high_turns == 0 (position interpolation)  f'_i = f_i / factor
+ *   high_turns > low_turns >= 0 (by the turns that frequency i makes in
+ *     original_len tokens, n_i = original_len f_i / (2 pi)):
+ *     b_i = clamp((n_i - low_turns) / (high_turns - low_turns), 0, 1)
+ *     f'_i = (1 - b_i) f_i / factor + b_i f_i
+ *   table [n_pos x rot_dim/2 x 2] float, device, out, 16-byte aligned.
+ *   rot_dim a positive multiple of 16 up to 256; theta > 0; factor > 0;
+ *   first_pos >= 0; first_pos + n_pos <= 2^31. n_pos == 0 is a no-op. */
+typedef struct sq_rope_scaling {
+    double factor;
+    double low_turns;
+    double high_turns;
+    int64_t original_len;
+    double magnitude;
+} sq_rope_scaling;
+sq_status sq_rope_table(float* table, int64_t first_pos, int64_t n_pos, int64_t rot_dim, double theta,
+                        const sq_rope_scaling* scaling, sq_stream_t stream);
+
+/* ---------------------------------------------------------------- 8-bit key/value cache
+ * A paged cache of symmetric int8 codes (the same [-127, 127] codes as the
+ * projections') with one fp32 scale for each block of scale_block consecutive
+ * tokens and head; value = code * scale.
+ *   k, v              [n_pages x n_heads x page_size x head_dim] int8
+ *   k_scale, v_scale  [n_pages x n_heads x page_size / scale_block] float
+ * all device memory of the caller, 16-byte aligned. head_dim 64 or 128;
+ * page_size 16, 32, 64 or 128; scale_block a power of two <= page_size;
+ * n_heads (of keys and values) 1 .. 1024. The struct itself is host memory and
+ * is read during the call only.
+ *
+ * Sequence b's token at position p is in page block_table[b * max_pages + p /
+ * page_size], slot p % page_size. block_table [n_seqs x max_pages] int32,
+ * device; entries behind a sequence's last token are not read. A page number
+ * outside [0, n_pages), a length beyond max_pages * page_size and a negative
+ * length are found on the device: the access is skipped, sq_get_status()
+ * reports SQ_ERR_BOUNDS, and outputs that depend on it are NaN (where a call
+ * says nothing else). max_pages * page_size <= 2^30.
+ * n_seqs <= 65536 for every call. */
+typedef struct sq_kv_cache {
+    int8_t* k;
+    int8_t* v;
+    float* k_scale;
+    float* v_scale;
+    int64_t n_pages;
+    int32_t n_heads;
+    int32_t head_dim;
+    int32_t page_size;
+    int32_t scale_block;
+} sq_kv_cache;
+
+/* sq_rope_kv_append: rotate q and k and append k and v to the cache.
+ *   Row t of q, k and v is token t - cu_new[b] of the new tokens of the
+ *   sequence b with cu_new[b] <= t < cu_new[b+1]; its position is
+ *   p = ctx_len[b] + t - cu_new[b].
+ *   q^ = R_p q, k^ = R_p k: for i < rot_dim / 2 the channels (i, i + rot_dim/2),
+ *   or (2i, 2i + 1) with interleaved != 0, become
+ *     (RN(RN(a c) - RN(b s)), RN(RN(b c) + RN(a s))),  (c, s) = table[p, i];
+ *   channels from rot_dim on stay as they are.
+ *   For every block of scale_block positions that receives tokens, head, and
+ *   each of k^ and v:
+ *     s_old = the block's scale if it holds earlier tokens (positions below
+ *             ctx_len[b]), else 0
+ *     s     = max(s_old, RN(max |new values of the block| / 127))
+ *     code  = clamp(round(RN(value / s)), -127, 127)           (0 if s = 0)
+ *     earlier tokens' codes = clamp(round(RN(RN(code * s_old) / s)), -127, 127)
+ *   so a block's scale only grows while it fills, and each growth moves the
+ *   values already held by at most half a step of the new scale. Codes that
+ *   were not written yet stay as they were. With scale_block = 1 every token
+ *   keeps its own scale and no code is written twice.
+ *   q [T x n_q_heads x head_dim], k, v [T x n_heads x head_dim]: dtype dt (SQ_F32 or
+ *     SQ_BF16), device, finite values. Heads are contiguous; tokens are
+ *     q_stride, k_stride, v_stride elements apart (slices of one QKV output),
+ *     each a multiple of 16 bytes. q may be NULL with n_q_heads 0.
+ *   q_out [T x n_q_heads x head_dim], k_out [T x n_heads x head_dim]: dtype dt,
+ *     contiguous, the rotated q and (unquantized) k, rounded once; k_out may be
+ *     NULL. q_out may be q and k_out may be k when that tensor is contiguous
+ *     (each thread writes only what it read); no other aliasing.
+ *   table: as from sq_rope_table with first_pos 0, n_pos rows; NULL with
+ *     rot_dim 0 for no rotation. rot_dim a multiple of 16, <= head_dim.
+ *   cu_new [n_seqs + 1] int32, ascending from 0, device; rows from
+ *     cu_new[n_seqs] on are neither read nor written (a padded batch).
+ *   ctx_len [n_seqs] int32, device: tokens the sequence holds already. The call does
+ *     not change it.
+ *   A page that receives tokens must belong to one sequence of the call. A
+ *   position beyond the table or the block table is not appended and gives NaN
+ *   in q_out and k_out. T <= 2^30, n_q_heads <= 1024. */
+sq_status sq_rope_kv_append(const sq_kv_cache* cache, const int32_t* block_table, int64_t max_pages,
+                            const int32_t* ctx_len, const int32_t* cu_new, int64_t n_seqs, int64_t T,
+                            const void* q, int64_t q_stride, int64_t n_q_heads, const void* k, int64_t k_stride,
+                            const void* v, int64_t v_stride, sq_dtype dt, const float* table, int64_t n_pos,
+                            int64_t rot_dim, int interleaved, void* q_out, void* k_out, sq_stream_t stream);
+
+/* sq_kv_read: cached tokens as values. Row r of the outputs is position
+ *   first[b] + r - cu_out[b] of the sequence b with cu_out[b] <= r < cu_out[b+1],
+ *     out = RN(code * scale), rounded once more for SQ_BF16.
+ *   first [n_seqs], cu_out [n_seqs + 1] int32, device; T rows in the outputs; rows from
+ *   cu_out[n_seqs] on are left as they were.
+ *   k_out, v_out [T x n_heads x head_dim], dtype dt (SQ_F32 or SQ_BF16), contiguous. */
+sq_status sq_kv_read(const sq_kv_cache* cache, const int32_t* block_table, int64_t max_pages, const int32_t* first,
+                     const int32_t* cu_out, int64_t n_seqs, int64_t T, void* k_out, void* v_out, sq_dtype dt,
+                     sq_stream_t stream);
+
+/* sq_kv_attention: the newest q_len tokens of every sequence attend to its
+ *   cached tokens, themselves included:
+ *     out[b, i, h] = sum_p softmax_p(scale * q[b, i, h] . K[p, h/g]) V[p, h/g],
+ *     p = 0 .. seq_len[b] - q_len + i,   g = n_q_heads / n_heads,
+ *     lse[b, i, h] = log sum_p exp(scale * q . K[p])
+ *   K and V the values that the cache holds. Query row i of a sequence shorter than
+ *   q_len - i sees nothing: out 0, lse -infinity (seq_len[b] = 0 pads a batch).
+ *   q [n_seqs x q_len x n_q_heads x head_dim], dtype dt (SQ_F32 or SQ_BF16); rows of
+ *     (sequence, query token) are q_stride elements apart (a multiple of 16 bytes).
+ *   out [n_seqs x q_len x n_q_heads x head_dim], dtype dt, contiguous.
+ *   lse [n_seqs x q_len x n_q_heads] float or NULL.
+ *   seq_len [n_seqs] int32, device: tokens in the cache, the new ones among them.
+ *   n_q_heads a multiple of n_heads; q_len * g <= 128; finite q; scale finite.
+ *   bf16 q is exact in the products (fp16 after a power-of-two scale, what
+ *   rounds is below 2^-24 of the row's largest value), fp32 q is split in two
+ *   fp16 parts; sums, maxima and accumulators are fp32; the probabilities are
+ *   rounded to fp16 (two fp16 parts for fp32 q).
+ *   workspace: device, 256-byte aligned, ws_bytes >= sq_kv_attention_workspace_size(...)
+ *     on the same device; it needs no initialisation and holds nothing between
+ *     calls. Calls that share one must not overlap on the GPU. */
+size_t sq_kv_attention_workspace_size(const sq_kv_cache* cache, int64_t n_seqs, int64_t q_len, int64_t n_q_heads);
+sq_status sq_kv_attention(const void* q, int64_t q_stride, sq_dtype dt, const sq_kv_cache* cache,
+                          const int32_t* block_table, int64_t max_pages, const int32_t* seq_len, int64_t n_seqs,
+                          int64_t q_len, int64_t n_q_heads, float scale, void* out, float* lse, void* workspace,
+                          size_t ws_bytes, sq_stream_t stream);
+
+/* ---------------------------------------------------------------- attention over prompts
+ * sq_prompt_attention: packed sequences attend to themselves,
+ *     out[t, h] = sum_u softmax_u(scale * q[t, h] . k[u, h/g]) v[u, h/g]
+ *   over the tokens u of t's sequence (u <= t if causal), g = n_q_heads / n_kv_heads.
+ *   Sequence b is rows cu_seqlens[b] .. cu_seqlens[b+1] - 1; cu_seqlens
+ *   [n_seqs + 1] int32, ascending from 0, device. Rows from cu_seqlens[n_seqs] on are
+ *   left as they were; what lies in those rows of q, k and v never matters.
+ *   q [T x n_q_heads x head_dim], k, v [T x n_kv_heads x head_dim], bf16, device;
+ *   heads contiguous, tokens q_stride, k_stride, v_stride elements apart
+ *   (multiples of 8). out [T x n_q_heads x head_dim] bf16 contiguous;
+ *   lse [T x n_q_heads] float or NULL: log sum exp of the row's scaled scores.
+ *   head_dim 64 or 128. Scores and sums in fp32; probabilities are rounded to
+ *   bf16 for the second product. A sequence's own values must be finite.
+ *   Offsets outside [0, T] or descending are cut, and sq_get_status() reports SQ_ERR_BOUNDS.
+ *   T <= 2^30 / n_q_heads, n_seqs <= 65536. */
+sq_status sq_prompt_attention(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
+                              int64_t v_stride, const int32_t* cu_seqlens, int64_t n_seqs, int64_t T,
+                              int64_t n_q_heads, int64_t n_kv_heads, int64_t head_dim, float scale, int causal,
+                              void* out, float* lse, sq_stream_t stream);
 
 /* ---------------------------------------------------------------- measurement aid
  * sq_probe_tensor_int8: the int8 tensor-core rate of the current GPU, as a

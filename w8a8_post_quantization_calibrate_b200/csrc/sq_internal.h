@@ -87,6 +87,12 @@ enum Site : unsigned int {
     SITE_DBG_RING_SCALE = 52,
     SITE_DBG_GEMM_VECTOR = 53,
     SITE_DBG_DECODE_OWNER = 54,
+    SITE_KV_APPEND = 60,
+    SITE_KV_READ = 61,
+    SITE_KV_ATTENTION = 62,
+    SITE_KV_ATTENTION_WAIT = 63,
+    SITE_PROMPT = 64,
+    SITE_PROMPT_WAIT = 65,
 };
 
 // Internal entry points used by sq_linear.

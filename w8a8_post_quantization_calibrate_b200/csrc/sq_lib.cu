@@ -9,3 +9,6 @@
 #include "sq_split.cu"
 #include "sq_gemm_noalloc.cu"
 #include "sq_search.cu"
+#include "sq_kv.cu"
+#include "sq_kv_attention.cu"
+#include "sq_prompt_attention.cu"

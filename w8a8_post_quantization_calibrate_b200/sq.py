@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import typing
 
 import torch
 
@@ -68,6 +69,14 @@ _SIGS = {
     "sq_linear_workspace_size": ([_i64, _i64, _i64, _int, _int], _sz),
     "sq_linear_workspace_offsets": ([_i64, _i64, _i64, _int, _int, _vp], _int),
     "sq_linear": ([_vp, _vp, _int, _i64, _i64, _i64, _f32, _f32, _vp, _int, _vp, _sz, _vp], _int),
+    "sq_rope_table": ([_vp, _i64, _i64, _i64, ctypes.c_double, _vp, _vp], _int),
+    "sq_rope_kv_append": ([_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _i64, _i64, _vp, _i64, _vp, _i64, _int, _vp, _i64,
+                           _i64, _int, _vp, _vp, _vp], _int),
+    "sq_kv_read": ([_vp, _vp, _i64, _vp, _vp, _i64, _i64, _vp, _vp, _int, _vp], _int),
+    "sq_kv_attention_workspace_size": ([_vp, _i64, _i64, _i64], _sz),
+    "sq_kv_attention": ([_vp, _i64, _int, _vp, _vp, _i64, _vp, _i64, _i64, _i64, _f32, _vp, _vp, _vp, _sz, _vp], _int),
+    "sq_prompt_attention": ([_vp, _i64, _vp, _i64, _vp, _i64, _vp, _i64, _i64, _i64, _i64, _i64, _f32, _int, _vp, _vp,
+                             _vp], _int),
     "sq_get_status": ([_vp], _int),
     "sq_last_status_site": ([], ctypes.c_uint),
     "sq_last_error_string": ([], ctypes.c_char_p),
@@ -525,6 +534,264 @@ def sq_linear(x: torch.Tensor, w: torch.Tensor, alpha: float, eps: float = 1e-8,
                           y.data_ptr(), _dt(y), workspace.data_ptr(), workspace.numel(), _stream(stream)),
            "sq_linear")
     return y
+
+
+class _RopeScaling(ctypes.Structure):
+    _fields_ = [("factor", ctypes.c_double), ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
+                ("original_len", _i64), ("magnitude", ctypes.c_double)]
+
+
+class _KvCacheStruct(ctypes.Structure):
+    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("n_pages", _i64),
+                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
+                ("scale_block", ctypes.c_int32)]
+
+
+class KvCache(typing.NamedTuple):
+    """A paged 8-bit key/value cache (sq_kv_cache): int8 codes k, v [n_pages,
+    n_heads, page_size, head_dim] and float32 scales k_scale, v_scale [n_pages,
+    n_heads, page_size / scale_block], one per scale_block tokens and head."""
+    k: torch.Tensor
+    v: torch.Tensor
+    k_scale: torch.Tensor
+    v_scale: torch.Tensor
+
+    @classmethod
+    def empty(cls, n_pages: int, n_heads: int, head_dim: int, page_size: int = 64, scale_block: int = 16, device="cuda"):
+        """A cache that holds nothing yet (codes and scales uninitialised)."""
+        codes = [torch.empty((n_pages, n_heads, page_size, head_dim), dtype=torch.int8, device=device) for _ in range(2)]
+        scales = [torch.empty((n_pages, n_heads, page_size // scale_block), dtype=torch.float32, device=device)
+                  for _ in range(2)]
+        return cls(*codes, *scales)
+
+
+def _cache_struct(cache: KvCache) -> _KvCacheStruct:
+    k, v, ks, vs = cache
+    n_pages, n_heads, page_size, head_dim = k.shape
+    if v.shape != k.shape or vs.shape != ks.shape or ks.dim() != 3 or ks.shape[:2] != k.shape[:2]:
+        raise ValueError("cache: k and v, and k_scale and v_scale, must have the same shapes")
+    blocks = ks.shape[2]
+    if blocks == 0 or page_size % blocks:
+        raise ValueError("cache: page_size must be a multiple of the scales per page")
+    if k.dtype != torch.int8 or v.dtype != torch.int8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
+        raise TypeError("cache: codes are int8, scales float32")
+    return _KvCacheStruct(_dev(k, "cache.k"), _dev(v, "cache.v"), _dev(ks, "cache.k_scale"), _dev(vs, "cache.v_scale"),
+                          n_pages, n_heads, head_dim, page_size, page_size // blocks)
+
+
+def _same_device(first: torch.Tensor, *others) -> None:
+    for t in others:
+        if t is not None and t.device != first.device:
+            raise ValueError(f"tensors on {first.device} and {t.device}")
+
+
+def _i32(t: torch.Tensor, shape: tuple, name: str) -> int:
+    if t.dtype != torch.int32:
+        raise TypeError(f"{name} must be int32")
+    if tuple(t.shape) != shape:
+        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
+    return _dev(t, name)
+
+
+def _token_rows(t: torch.Tensor, name: str) -> tuple[int, int]:
+    """(address, elements between tokens) of [.., tokens, heads, head_dim] whose
+    heads are contiguous and whose tokens are evenly spaced."""
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    shape, stride = t.shape, t.stride()
+    if t.numel() and ((shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1])):
+        raise ValueError(f"{name}: the heads of a token must be contiguous")
+    width = shape[-1] * shape[-2]
+    step = stride[-3] if shape[-3] > 1 else width
+    if t.dim() == 4 and shape[0] > 1:
+        if shape[1] == 1:
+            step = stride[0]
+        elif stride[0] != shape[1] * step:
+            raise ValueError(f"{name}: tokens must be evenly spaced")
+    return t.data_ptr(), step
+
+
+def _made(shape, dtype, device, stream) -> torch.Tensor:
+    """A tensor that the call on `stream` writes; known to the allocator as in
+    use there when that is not the current stream."""
+    t = torch.empty(shape, dtype=dtype, device=device)
+    if stream is not None:
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+    return t
+
+
+class _on:
+    """Makes `device` current for a call if it is not, and gives its stream."""
+
+    def __init__(self, device: torch.device, stream):
+        index = device.index if device.index is not None else torch.cuda.current_device()
+        self.guard = torch.cuda.device(index) if index != torch.cuda.current_device() else None
+        self.stream = stream
+
+    def __enter__(self) -> int:
+        if self.guard is not None:
+            self.guard.__enter__()
+        return _stream(self.stream)
+
+    def __exit__(self, *args):
+        if self.guard is not None:
+            self.guard.__exit__(*args)
+
+
+def sq_rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, first_pos: int = 0, factor: float = 1.0,
+                  low_turns: float = 0.0, high_turns: float = 0.0, original_len: int = 0, magnitude: float = 1.0,
+                  table: torch.Tensor | None = None, device=None, stream=None) -> torch.Tensor:
+    """cos and sin of the rotary angles, float32 [n_pos, rot_dim / 2, 2];
+    frequencies scaled by `factor`, all of them or (high_turns > 0) those that
+    make few turns in original_len tokens."""
+    device = table.device if table is not None else torch.device("cuda" if device is None else device)
+    if device.type != "cuda":
+        raise ValueError("the table is a CUDA tensor")
+    if table is not None and (tuple(table.shape) != (n_pos, rot_dim // 2, 2) or table.dtype != torch.float32):
+        raise ValueError(f"table must be float32 [{n_pos}, {rot_dim // 2}, 2]")
+    scaling = _RopeScaling(float(factor), float(low_turns), float(high_turns), int(original_len), float(magnitude))
+    with _on(device, stream) as st:
+        if table is None:
+            table = _made((max(n_pos, 0), max(rot_dim, 0) // 2, 2), torch.float32, device, stream)
+        _check(_lib.sq_rope_table(_dev(table, "table"), first_pos, n_pos, rot_dim, float(theta), ctypes.byref(scaling), st),
+               "sq_rope_table")
+    return table
+
+
+def sq_rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, cache: KvCache, block_table: torch.Tensor,
+                      ctx_len: torch.Tensor, cu_new: torch.Tensor, table: torch.Tensor | None = None,
+                      interleaved: bool = False, q_out: torch.Tensor | None = None, k_out: torch.Tensor | None = None,
+                      want_k: bool = False, stream=None):
+    """Rotate q [T, n_q_heads, head_dim] and k, append k and v [T, n_heads,
+    head_dim] to the cache -> (rotated q, rotated k or None). The tensors may be
+    slices of one QKV output."""
+    c = _cache_struct(cache)
+    T = k.shape[0]
+    if k.shape != v.shape or tuple(k.shape) != (T, c.n_heads, c.head_dim):
+        raise ValueError(f"k and v must be [T, {c.n_heads}, {c.head_dim}]")
+    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
+        raise TypeError("q, k and v must have the same dtype")
+    _same_device(k, q, v, *cache, block_table, ctx_len, cu_new, table, q_out, k_out)
+    n_seqs, max_pages = block_table.shape
+    dt = _dt(k)
+    with _on(k.device, stream) as st:
+        q_ptr, q_step, hq, qo = None, 0, 0, None
+        if q is not None:
+            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != c.head_dim:
+                raise ValueError(f"q must be [{T}, n_q_heads, {c.head_dim}]")
+            hq = q.shape[1]
+            q_ptr, q_step = _token_rows(q, "q")
+            if q_out is None:
+                q_out = _made((T, hq, c.head_dim), q.dtype, q.device, stream)
+            elif q_out.shape != q.shape or q_out.dtype != q.dtype:
+                raise ValueError("q_out must have q's shape and dtype")
+            qo = _dev(q_out, "q_out")
+        k_ptr, k_step = _token_rows(k, "k")
+        v_ptr, v_step = _token_rows(v, "v")
+        if k_out is None and want_k:
+            k_out = _made((T, c.n_heads, c.head_dim), k.dtype, k.device, stream)
+        elif k_out is not None and (k_out.shape != k.shape or k_out.dtype != k.dtype):
+            raise ValueError("k_out must have k's shape and dtype")
+        t_ptr, n_pos, rot = None, 0, 0
+        if table is not None:
+            if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
+                raise ValueError("table must be float32 [n_pos, rot_dim / 2, 2]")
+            t_ptr, n_pos, rot = _dev(table, "table"), table.shape[0], 2 * table.shape[1]
+        _check(_lib.sq_rope_kv_append(ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"), max_pages,
+                                      _i32(ctx_len, (n_seqs,), "ctx_len"), _i32(cu_new, (n_seqs + 1,), "cu_new"), n_seqs, T,
+                                      q_ptr, q_step, hq, k_ptr, k_step, v_ptr, v_step, dt, t_ptr, n_pos, rot,
+                                      int(interleaved), qo, _opt_dev(k_out, "k_out"), st), "sq_rope_kv_append")
+    return q_out, k_out
+
+
+def sq_kv_read(cache: KvCache, block_table: torch.Tensor, first: torch.Tensor, cu_out: torch.Tensor, n_rows: int,
+               dtype=torch.bfloat16, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
+    """The cached tokens from first[b] on of every sequence, packed by cu_out
+    into n_rows rows -> (k, v) [n_rows, n_heads, head_dim]."""
+    c = _cache_struct(cache)
+    _same_device(cache.k, *cache[1:], block_table, first, cu_out, k_out, v_out)
+    n_seqs, max_pages = block_table.shape
+    shape = (n_rows, c.n_heads, c.head_dim)
+    with _on(cache.k.device, stream) as st:
+        if k_out is None:
+            k_out = _made(shape, dtype, cache.k.device, stream)
+        if v_out is None:
+            v_out = _made(shape, k_out.dtype, cache.k.device, stream)
+        if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or k_out.dtype != v_out.dtype:
+            raise ValueError(f"k_out and v_out must be {shape} and of one dtype")
+        _check(_lib.sq_kv_read(ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"), max_pages,
+                               _i32(first, (n_seqs,), "first"), _i32(cu_out, (n_seqs + 1,), "cu_out"), n_seqs, n_rows,
+                               _dev(k_out, "k_out"), _dev(v_out, "v_out"), _dt(k_out), st), "sq_kv_read")
+    return k_out, v_out
+
+
+def sq_kv_attention_workspace_size(cache: KvCache, n_seqs: int, q_len: int, n_q_heads: int) -> int:
+    with _on(cache.k.device, None):
+        return int(_lib.sq_kv_attention_workspace_size(ctypes.byref(_cache_struct(cache)), n_seqs, q_len, n_q_heads))
+
+
+def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_len: torch.Tensor,
+                    scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                    want_lse: bool = False, workspace: torch.Tensor | None = None, stream=None):
+    """The newest q_len tokens' q [n_seqs, q_len, n_q_heads, head_dim] over the
+    cached tokens of their sequences -> out, or (out, lse) if asked for. `scale`
+    is head_dim ** -0.5 if not given."""
+    c = _cache_struct(cache)
+    if q.dim() != 4 or q.shape[3] != c.head_dim:
+        raise ValueError(f"q must be [n_seqs, q_len, n_q_heads, {c.head_dim}]")
+    n_seqs, q_len, hq, d = q.shape
+    max_pages = block_table.shape[1]
+    _same_device(q, *cache, block_table, seq_len, out, lse, workspace)
+    dt = _dt(q)
+    with _on(q.device, stream) as st:
+        q_ptr, q_step = _token_rows(q, "q")
+        if out is None:
+            out = _made((n_seqs, q_len, hq, d), q.dtype, q.device, stream)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and dtype")
+        if lse is None and want_lse:
+            lse = _made((n_seqs, q_len, hq), torch.float32, q.device, stream)
+        elif lse is not None and (tuple(lse.shape) != (n_seqs, q_len, hq) or lse.dtype != torch.float32):
+            raise ValueError("lse must be float32 [n_seqs, q_len, n_q_heads]")
+        if workspace is None:
+            need = int(_lib.sq_kv_attention_workspace_size(ctypes.byref(c), n_seqs, q_len, hq))
+            workspace = _made((need,), torch.uint8, q.device, stream)
+        _check(_lib.sq_kv_attention(q_ptr, q_step, dt, ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"),
+                                    max_pages, _i32(seq_len, (n_seqs,), "seq_len"), n_seqs, q_len, hq,
+                                    float(d ** -0.5 if scale is None else scale), _dev(out, "out"), _opt_dev(lse, "lse"),
+                                    _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), st),
+               "sq_kv_attention")
+    return out if lse is None else (out, lse)
+
+
+def sq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_seqlens: torch.Tensor, causal: bool = True,
+                        scale: float | None = None, out: torch.Tensor | None = None, lse: torch.Tensor | None = None,
+                        want_lse: bool = False, stream=None):
+    """Packed prompts q [T, n_q_heads, head_dim], k, v [T, n_kv_heads, head_dim]
+    (bf16; slices of one QKV output may be given) over themselves -> out, or
+    (out, lse) if asked for. `scale` is head_dim ** -0.5 if not given."""
+    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+        raise ValueError("q must be [T, n_q_heads, head_dim], k and v [T, n_kv_heads, head_dim]")
+    if any(t.dtype != torch.bfloat16 for t in (q, k, v)):
+        raise TypeError("q, k and v must be bfloat16")
+    _same_device(q, k, v, cu_seqlens, out, lse)
+    T, hq, d = q.shape
+    n_seqs = cu_seqlens.shape[0] - 1
+    (q_ptr, q_step), (k_ptr, k_step), (v_ptr, v_step) = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
+    with _on(q.device, stream) as st:
+        if out is None:
+            out = _made((T, hq, d), q.dtype, q.device, stream)
+        elif out.shape != q.shape or out.dtype != q.dtype:
+            raise ValueError("out must have q's shape and dtype")
+        if lse is None and want_lse:
+            lse = _made((T, hq), torch.float32, q.device, stream)
+        elif lse is not None and (tuple(lse.shape) != (T, hq) or lse.dtype != torch.float32):
+            raise ValueError("lse must be float32 [T, n_q_heads]")
+        _check(_lib.sq_prompt_attention(q_ptr, q_step, k_ptr, k_step, v_ptr, v_step,
+                                        _i32(cu_seqlens, (n_seqs + 1,), "cu_seqlens"), n_seqs, T, hq, k.shape[1], d,
+                                        float(d ** -0.5 if scale is None else scale), int(causal), _dev(out, "out"),
+                                        _opt_dev(lse, "lse"), st), "sq_prompt_attention")
+    return out if lse is None else (out, lse)
 
 
 def sq_get_status(stream=None) -> int:
