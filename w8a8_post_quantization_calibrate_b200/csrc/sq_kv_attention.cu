@@ -1,6 +1,8 @@
 // sq_kv_attention.cu -- attention of the newest tokens over the paged 8-bit
 // cache (sq_kv_attention). Included into the library's single translation unit
 // after sq_kv.cu, whose cache view and argument checks it uses.
+#include <cuda.h>
+#include <cuda_fp16.h>
 #include <cuda_runtime.h>
 
 #include "sq_device.cuh"
@@ -23,55 +25,692 @@ struct KvAttnArgs {
     const void* q;
     void* out;
     float* lse;
+    long long wait_limit;
+    int64_t* work;      // in the workspace: the number of tiles,
+    int4* start;        // where each CTA begins (sequence, head, tile, tiles of the sequence),
+    float2* part_ml;    // and two partial results of each CTA
+    float* part_o;
 };
 
-// One warp for each (sequence, query token, query head); a lane holds D / 32
-// channels, and the softmax runs along the tokens.
+// The kernel. Every key/value head's G = n_q_heads / n_heads query heads times q_len query
+// tokens are R rows that share its keys: reading the codes is the floor, so
+// they go from HBM through a ring of shared-memory stages (TMA, one page
+// of one head a copy) once per head, whatever R is.
+//   Work: tiles of 128 tokens, numbered by sequence, head, tile. The CTAs, one on each
+// SM, take equal shares of all W tiles, wherever the sequences' borders fall, so a
+// ragged batch is balanced without the host knowing a length. A (sequence, head)
+// that several CTAs share leaves one partial result (reference, sum, accumulator) from
+// each in the workspace; a second small kernel joins them in a fixed order.
+//   Inside a CTA eight warps take 16 tokens of a tile each (with more than 16 rows, MT row
+// tiles times 8 / MT token groups), with a softmax reference, sum and accumulator
+// of their own that meet once at the end of a head's piece: no barrier
+// between warps inside the loop.
+//   S = Q K^T and O += P V are m16n8k16 products with fp32 accumulators (rows
+// x tokens, rows x channels). The channels of a k step may come in any order as
+// long as Q and K agree, and the columns of S may be any tokens: the orders
+// here are those in which one 16-byte shared-memory read gives a lane its codes
+// without bank conflicts, and S's accumulators are P's operand registers as they lie.
+//   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
+//   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
+// w = 2^(s - m) vs, with the reference m at least the largest s + floor(log2 vs) less 8,
+// so that w stays inside fp16's normal range for scales of any size; the sum takes 2^(s - m).
+// References move only when a score is 2^8 above, which is rare after the first tiles.
+constexpr int kTile = 128;
+constexpr int kConsumers = 8;
+constexpr int kAttnThreads = 32 * (kConsumers + 1);
+constexpr float kSlack = 8.0f;
+constexpr float kNoScale = -80.0f;   // exponent that stands for scales below 2^-80: 2^88 times 2^30 tokens is finite
+
+template <int D>
+struct AttnSmem {
+    static constexpr int STAGES = D == 128 ? 4 : 6;
+    static constexpr int CODES = kTile * D;                   // bytes of K, and of V
+    static constexpr int STAGE = 2 * CODES + 2 * kTile * 4;   // and their scales
+    static constexpr int ROW = D + 16;                        // floats of a merge row: D with a gap of 4 in each quarter
+    static constexpr int MERGE = kConsumers * 16 * ROW * 4;
+    static constexpr int TOTAL = 1024 + STAGES * STAGE + MERGE;
+};
+
+__device__ __forceinline__ uint32_t lop_and_xor(uint32_t x, uint32_t m, uint32_t c) {
+    uint32_t r;
+    asm("lop3.b32 %0, %1, %2, %3, 0x6a;" : "=r"(r) : "r"(x), "r"(m), "r"(c));   // (x & m) ^ c
+    return r;
+}
+__device__ __forceinline__ uint32_t sub_1152(uint32_t h) {
+    const __half2 r = __hsub2(*reinterpret_cast<__half2*>(&h), __half2half2(__ushort_as_half(0x6480)));
+    return *reinterpret_cast<const uint32_t*>(&r);
+}
+// Codes (0, 2) and (1, 3) of a word as fp16 pairs.
+__device__ __forceinline__ void codes_even_odd(uint32_t w, uint32_t& even, uint32_t& odd) {
+    even = sub_1152(lop_and_xor(w, 0x00ff00ffu, 0x64806480u));
+    odd = sub_1152(lop_and_xor(w >> 8, 0x00ff00ffu, 0x64806480u));
+}
+// Code i of a and of b as an fp16 pair.
+template <int I>
+__device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b) {
+    return sub_1152(lop_and_xor(__byte_perm(a, b, (4 + I) << 8 | I), 0x00ff00ffu, 0x64806480u));
+}
+__device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    const __half2 h = __floats2half2_rn(lo, hi);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// What fp16 leaves of a pair, as an fp16 pair.
+__device__ __forceinline__ uint32_t rest_f16x2(float lo, float hi, uint32_t packed) {
+    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&packed));
+    return pack_f16x2(lo - f.x, hi - f.y);
+}
+__device__ __forceinline__ float exp2_fast(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ uint4 lds128(uint32_t a) {
+    uint4 r;
+    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];" : "=r"(r.x), "=r"(r.y), "=r"(r.z), "=r"(r.w) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ uint2 lds64(uint32_t a) {
+    uint2 r;
+    asm volatile("ld.shared.v2.u32 {%0,%1}, [%2];" : "=r"(r.x), "=r"(r.y) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ float lds32(uint32_t a) {
+    float r;
+    asm volatile("ld.shared.f32 %0, [%1];" : "=f"(r) : "r"(a));
+    return r;
+}
+__device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint32_t bar, int32_t x, int32_t y, int32_t z) {
+    asm volatile(
+        "cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes"
+        " [%0], [%1, {%3, %4, %5}], [%2];"
+        :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
+}
+__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
+}
+__device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
+}
+
+// A sequence's tokens, -1 if its length is impossible.
+__device__ __forceinline__ int attn_len(const KvAttnArgs& g, int b) {
+    const int n = __ldg(g.seq_len + b);
+    return n < 0 || n > (g.max_pages << g.c.page_shift) ? -1 : n;
+}
+__device__ __forceinline__ int tiles_of(int len) { return len > 0 ? (len + kTile - 1) / kTile : 0; }
+
+// Where a CTA is in the numbering; producer and consumers walk it alike.
+struct TileWalk {
+    int b, h, tile, nt, len;
+    __device__ __forceinline__ void next(const KvAttnArgs& g) {
+        if (++tile < nt) return;
+        tile = 0;
+        if (++h < g.c.n_heads) return;
+        h = 0;
+        do {
+            len = attn_len(g, ++b);
+            nt = tiles_of(len);
+        } while (nt == 0);   // only called while tiles remain, so a later sequence has some
+    }
+};
+
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kConsumers) : "memory"); }
+
+// Four channels of a finished row.
 template <typename T, int D>
-__global__ void __launch_bounds__(128) kv_attention_kernel(const KvAttnArgs g) {
-    constexpr int E = D / 32;
+__device__ __forceinline__ void attn_result(const KvAttnArgs& g, int b, int h, int row, int G, int d, float4 acc, float M, float L) {
+    const int64_t at = ((int64_t)b * g.q_len + row / G) * g.n_q_heads + h * G + row % G;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;   // NaN stays NaN
+    T* o = static_cast<T*>(g.out) + at * D + d;
+    if constexpr (sizeof(T) == 4)
+        *reinterpret_cast<float4*>(o) = make_float4(acc.x * inv, acc.y * inv, acc.z * inv, acc.w * inv);
+    else
+        *reinterpret_cast<uint2*>(o) = make_uint2(pack_bf16x2(acc.x * inv, acc.y * inv), pack_bf16x2(acc.z * inv, acc.w * inv));
+    if (g.lse && d == 0) g.lse[at] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
+}
+
+template <typename T, int D, int MT>
+__global__ void __launch_bounds__(kAttnThreads, 1)
+kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs g) {
+    using S = AttnSmem<D>;
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int KS = D / 16, NT = D / 8, DB = D / 8;   // k steps of S, column tiles of O, codes a lane holds of a value row
+    constexpr int TG = kConsumers / MT;                  // token groups
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 * S::STAGES];
+    __shared__ int abort_flag, stage_bad[S::STAGES];
+    __shared__ int64_t scan[kAttnThreads / 32 + 1];
+    __shared__ int start_b;
+    __shared__ int64_t start_prefix;
+    __shared__ float2 meet[2][kConsumers][16];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    const uint32_t full = smem_u32(bars), empty = full + 8 * S::STAGES;
+    float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S::STAGES * S::STAGE);
+    if (tid == 0) {
+        for (int i = 0; i < S::STAGES; ++i) {
+            mbar_init(full + 8 * i, 33);   // the producer's lanes (scales) and its expected bytes
+            mbar_init(empty + 8 * i, kConsumers);
+        }
+        abort_flag = 0;
+        start_b = 0;
+        start_prefix = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    if (id >= (int64_t)g.n_seqs * g.q_len * g.n_q_heads) return;
-    const int h = (int)(id % g.n_q_heads);
-    const int64_t row = id / g.n_q_heads;
-    const int b = (int)(row / g.q_len), i = (int)(row % g.q_len);
-    int64_t len = __ldg(g.seq_len + b);
-    bool bad = len < 0 || len > (g.max_pages << g.c.page_shift);
-    len = bad ? 0 : len - g.q_len + 1 + i;
-    const T* q = static_cast<const T*>(g.q) + row * g.q_stride + (int64_t)h * D;
-    float x[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        x[e] = to_f32(q[lane * E + e]) * g.scale;
-        o[e] = 0.0f;
+
+    // All tiles, and the sequence in which this CTA's share begins: every thread
+    // sums a run of sequences, the run that holds the border is walked again.
+    const int run = (g.n_seqs + kAttnThreads - 1) / kAttnThreads;
+    const int s0 = min(g.n_seqs, tid * run), s1 = min(g.n_seqs, s0 + run);
+    int64_t mine = 0;
+    for (int b = s0; b < s1; ++b) mine += tiles_of(attn_len(g, b));
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t up = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += up;
     }
-    float m = -INFINITY, l = 0.0f;
-    const int hk = h / (g.n_q_heads / g.c.n_heads);
-    for (int64_t p = 0; p < len; ++p) {
-        const int64_t page = __ldg(g.block_table + b * g.max_pages + (p >> g.c.page_shift));
-        if ((uint64_t)page >= (uint64_t)g.c.n_pages) { bad = true; break; }
-        const int64_t ph = page * g.c.n_heads + hk;
-        const int slot = (int)(p & (g.c.page_size - 1));
-        const int64_t at = ((ph << g.c.page_shift) + slot) * D + lane * E;
-        const int64_t sa = (ph << (g.c.page_shift - g.c.block_shift)) + (slot >> g.c.block_shift);
-        float s = 0.0f;
-        for (int e = 0; e < E; ++e) s += x[e] * (float)g.c.k[at + e];
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        s *= g.c.k_scale[sa];
-        const float mn = fmaxf(m, s);
-        const float f = expf(m - mn), w = expf(s - mn);
-        m = mn;
-        l = l * f + w;
-        const float wv = w * g.c.v_scale[sa];
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + wv * (float)g.c.v[at + e];
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    if (tid == 0) {
+        int64_t sum = 0;
+        for (int i = 0; i < kAttnThreads / 32; ++i) {
+            const int64_t v = scan[i];
+            scan[i] = sum;
+            sum += v;
+        }
+        scan[kAttnThreads / 32] = sum;
     }
-    if (bad && lane == 0) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
-    const float nan = __int_as_float(0x7fc00000);
-    for (int e = 0; e < E; ++e)
-        put(static_cast<T*>(g.out) + (row * g.n_q_heads + h) * D + lane * E + e, bad ? nan : l > 0.0f ? o[e] / l : 0.0f);
-    if (g.lse && lane == 0) g.lse[row * g.n_q_heads + h] = bad ? nan : l > 0.0f ? m + logf(l) : -INFINITY;
+    __syncthreads();
+    const int H = g.c.n_heads;
+    const int64_t W = scan[kAttnThreads / 32] * H;
+    const int64_t x0 = W * blockIdx.x / gridDim.x, x1 = W * (blockIdx.x + 1) / gridDim.x;
+    {
+        int64_t before = (scan[warp] + incl - mine) * H;
+        if (x0 >= before && x0 < before + mine * H) {
+            for (int b = s0; b < s1; ++b) {
+                const int64_t n = (int64_t)tiles_of(attn_len(g, b)) * H;
+                if (x0 < before + n) {
+                    start_b = b;
+                    start_prefix = before;
+                    break;
+                }
+                before += n;
+            }
+        }
+    }
+    __syncthreads();
+    TileWalk w{start_b, 0, 0, 0, 0};
+    w.len = attn_len(g, w.b);
+    w.nt = tiles_of(w.len);
+    if (w.nt > 0) {
+        w.h = (int)((x0 - start_prefix) / w.nt);
+        w.tile = (int)((x0 - start_prefix) % w.nt);
+    }
+    if (tid == 0) {
+        if (blockIdx.x == 0) *g.work = W;
+        g.start[blockIdx.x] = make_int4(w.b, w.h, x0 < W ? w.tile : 0, w.nt);
+    }
+    const int G = g.n_q_heads / H, R = G * g.q_len;
+    // sequences without tiles: nothing seen, or a length that cannot be
+    for (int b = blockIdx.x; b < g.n_seqs; b += gridDim.x) {
+        const int len = attn_len(g, b);
+        if (tiles_of(len) > 0) continue;
+        const float v = len < 0 ? __int_as_float(0x7fc00000) : 0.0f;
+        if (len < 0 && tid == 0) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
+        T* o = static_cast<T*>(g.out) + (int64_t)b * g.q_len * g.n_q_heads * D;
+        for (int i = tid; i < g.q_len * g.n_q_heads * D; i += kAttnThreads) put(o + i, v);
+        if (g.lse)
+            for (int i = tid; i < g.q_len * g.n_q_heads; i += kAttnThreads)
+                g.lse[(int64_t)b * g.q_len * g.n_q_heads + i] = len < 0 ? v : -INFINITY;
+    }
+
+    const int64_t n_items = x1 - x0;
+    const long long limit = g.wait_limit;
+    volatile int* abort = &abort_flag;
+    if (warp == kConsumers) {
+        // ---------------------------------------------------------------- producer
+        const int ps = g.c.page_size, sh = g.c.page_shift, per = kTile >> sh;   // pages of a tile
+        auto page_of = [&](const TileWalk& v) {   // lane i: page i of the tile, -2 if it holds no token
+            const int64_t p = (int64_t)v.tile * kTile + ((int64_t)lane << sh);
+            return lane < per && p < v.len ? __ldg(g.block_table + v.b * g.max_pages + (p >> sh)) : -2;
+        };
+        int page = n_items > 0 ? page_of(w) : -2;
+        int64_t issued = 0;
+        int st = 0;
+        uint32_t parity = 0;
+        for (int64_t i = 0; i < n_items; ++i) {
+            TileWalk nx = w;
+            int next_page = -2;
+            if (i + 1 < n_items) {
+                nx.next(g);
+                next_page = page_of(nx);
+            }
+            if (i >= S::STAGES) {
+                bool go = true;
+                if (lane == 0) go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
+                if (!__shfl_sync(0xffffffffu, go, 0)) break;
+            }
+            const bool there = page != -2;
+            const bool good = (uint32_t)page < (uint64_t)g.c.n_pages;
+            const unsigned bad = __ballot_sync(0xffffffffu, there && !good);
+            const unsigned load = __ballot_sync(0xffffffffu, there && good);
+            const uint32_t dst = ring + st * S::STAGE;
+            const uint32_t bar = full + 8 * st;
+            if (lane == 0) {
+                stage_bad[st] = bad != 0;
+                if (bad) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
+                mbar_arrive_expect_tx(bar, (uint32_t)__popc(load) * 2u * (uint32_t)(ps * D));
+            }
+            __syncwarp();
+            if (there && good) {
+                const int z = page * H + w.h;
+                tma_load_3d(dst + lane * ps * D, &map_k, bar, 0, 0, z);
+                tma_load_3d(dst + S::CODES + lane * ps * D, &map_v, bar, 0, 0, z);
+            }
+            const int tokens = min(kTile, w.len - w.tile * kTile);
+#pragma unroll
+            for (int k = 0; k < kTile / 32; ++k) {
+                const int t = k * 32 + lane;
+                const int pg = __shfl_sync(0xffffffffu, page, t >> sh);
+                if (t < tokens && (uint32_t)pg < (uint64_t)g.c.n_pages) {
+                    const int64_t at = (((int64_t)pg * H + w.h) << (sh - g.c.block_shift)) + ((t & (ps - 1)) >> g.c.block_shift);
+                    cp_async4(dst + 2 * S::CODES + t * 4, g.c.k_scale + at);
+                    cp_async4(dst + 2 * S::CODES + kTile * 4 + t * 4, g.c.v_scale + at);
+                }
+            }
+            cp_async_arrive(bar);
+            ++issued;
+            w = nx;
+            page = next_page;
+            if (++st == S::STAGES) {
+                st = 0;
+                parity ^= 1u;
+            }
+        }
+        if (*abort) {   // a wait ran out: the copies in flight end before the shared memory goes
+            __shared__ int drain;
+            if (lane == 0) {
+                drain = 0;
+                for (int64_t i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
+                    mbar_wait(full + 8 * (int)(i % S::STAGES), (i / S::STAGES) & 1, limit, &drain, SITE_KV_ATTENTION_WAIT);
+            }
+            __syncwarp();
+        }
+        return;
+    }
+
+    // -------------------------------------------------------------------- consumers
+    const int gr = lane >> 2, t4 = lane & 3;
+    const int mt = warp % MT, grp = warp / MT;
+    const int pi_g = gr & 1 ? (gr + 4) & 7 : gr;          // the token of column gr: 0 5 2 7 4 1 6 3
+    const int tok_a = 2 * t4, tok_b = (2 * t4 + 5) & 7;   // and of columns 2 t4, 2 t4 + 1
+    uint32_t k_off[D / 64], v_off[2];
+    if (D == 128) {
+        k_off[0] = pi_g * 128 + ((t4 ^ pi_g) << 4);
+        k_off[D / 64 - 1] = pi_g * 128 + (((4 + t4) ^ pi_g) << 4);
+        v_off[0] = tok_a * 128 + ((gr ^ tok_a) << 4);
+        v_off[1] = tok_b * 128 + ((gr ^ tok_b) << 4);
+    } else {
+        k_off[0] = pi_g * 64 + ((t4 ^ (pi_g >> 1)) << 4);
+        v_off[0] = tok_a * 64 + ((((gr >> 1) ^ (tok_a >> 1)) << 4) | ((gr & 1) << 3));
+        v_off[1] = tok_b * 64 + ((((gr >> 1) ^ (tok_b >> 1)) << 4) | ((gr & 1) << 3));
+    }
+    uint32_t qh[KS][4], ql[F32 ? KS : 1][4];
+    float o[NT][4], m[2], l[2], qs[2];
+    int see[2];       // tokens that rows gr and gr + 8 see
+    int see_all = 0;  // and that every row of the tile sees
+    bool spoilt = false, began_before = false;
+    int st = 0, piece = 0;
+    uint32_t parity = 0;
+    for (int64_t i = 0; i < n_items; ++i) {
+        if (i == 0 || w.tile == 0) {   // a new piece: its queries
+            spoilt = false;
+            began_before = w.tile > 0;
+            see_all = w.len - g.q_len + 1;
+#pragma unroll
+            for (int n = 0; n < NT; ++n)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                m[r] = -INFINITY;
+                l[r] = 0.0f;
+                const int row = mt * 16 + gr + 8 * r;
+                const bool has = row < R;
+                const int qi = has ? row / G : 0, hq = w.h * G + (has ? row % G : 0);
+                see[r] = has ? max(0, w.len - g.q_len + 1 + qi) : 0;
+                const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + qi) * g.q_stride + (int64_t)hq * D;
+                float x[KS][4];
+                float top = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+#pragma unroll
+                    for (int half = 0; half < 2; ++half) {
+                        float v[8];
+                        Chunk<T>::load(q + 64 * c + 16 * t4 + 8 * half, v);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            x[4 * c + 2 * half + (e >> 2)][e & 3] = v[e];
+                            top = fmaxf(top, fabsf(v[e]));
+                        }
+                    }
+                }
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+                top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+                const int ex = top > 0.0f ? ilogbf(top) : 0;   // |q| 2^-ex < 2
+                qs[r] = scalbnf(g.scale * 1.4426950408889634f, ex);
+#pragma unroll
+                for (int ks = 0; ks < KS; ++ks) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) x[ks][e] = scalbnf(x[ks][e], -ex);
+                    // codes 0 and 2 of a word make the first pair of a k step, 1 and 3 the second
+                    qh[ks][r] = pack_f16x2(x[ks][0], x[ks][2]);
+                    qh[ks][2 + r] = pack_f16x2(x[ks][1], x[ks][3]);
+                    if (F32) {
+                        ql[F32 ? ks : 0][r] = rest_f16x2(x[ks][0], x[ks][2], qh[ks][r]);
+                        ql[F32 ? ks : 0][2 + r] = rest_f16x2(x[ks][1], x[ks][3], qh[ks][2 + r]);
+                    }
+                }
+            }
+        }
+        mbar_wait(full + 8 * st, parity, limit, abort, SITE_KV_ATTENTION_WAIT);
+        const uint32_t base = ring + st * S::STAGE;
+        if (stage_bad[st]) spoilt = true;
+#pragma unroll 1
+        for (int sub = 0; sub < MT; ++sub) {
+            const int t0 = (grp + TG * sub) * 16;          // first of the 16 tokens, in the tile
+            const int p0 = w.tile * kTile + t0;            // and in the sequence
+            if (p0 >= w.len) break;
+            float s[2][4];
+#pragma unroll
+            for (int j = 0; j < 2; ++j) {
+                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+#pragma unroll
+                for (int c = 0; c < D / 64; ++c) {
+                    const uint4 kw = lds128(base + (t0 + 8 * j) * D + k_off[c]);
+                    const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t b0, b1;
+                        codes_even_odd(ws[e], b0, b1);
+                        mma_f16(s[j], qh[4 * c + e], b0, b1);
+                        if (F32) mma_f16(s[j], ql[F32 ? 4 * c + e : 0], b0, b1);
+                    }
+                }
+            }
+            float vs[4], ve[4];   // the four tokens' value scales and their exponents
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const uint32_t a = base + 2 * S::CODES + (t0 + 8 * j + (e ? tok_b : tok_a)) * 4;
+                    const float ks = lds32(a);
+                    const float v = lds32(a + kTile * 4);
+                    vs[2 * j + e] = v;
+                    ve[2 * j + e] = fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), kNoScale);
+                    s[j][e] *= qs[0] * ks;
+                    s[j][2 + e] *= qs[1] * ks;
+                }
+            if (p0 + 16 > see_all) {   // the end of what some row sees
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        const int p = p0 + 8 * j + (e ? tok_b : tok_a);
+                        if (p >= see[0]) s[j][e] = -INFINITY;
+                        if (p >= see[1]) s[j][2 + e] = -INFINITY;
+                        if (p >= w.len) {   // its scales were not loaded
+                            vs[2 * j + e] = 0.0f;
+                            ve[2 * j + e] = kNoScale;
+                        }
+                    }
+            }
+            float top[2];
+#pragma unroll
+            for (int r = 0; r < 2; ++r)
+                top[r] = fmaxf(fmaxf(s[0][2 * r] + ve[0], s[0][2 * r + 1] + ve[1]), fmaxf(s[1][2 * r] + ve[2], s[1][2 * r + 1] + ve[3]));
+            if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+#pragma unroll
+                for (int r = 0; r < 2; ++r) {
+                    float x = top[r];
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                    x = fmaxf(x, m[r]);
+                    const float f = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - x);
+                    m[r] = x;
+                    l[r] *= f;
+#pragma unroll
+                    for (int n = 0; n < NT; ++n) {
+                        o[n][2 * r] *= f;
+                        o[n][2 * r + 1] *= f;
+                    }
+                }
+            }
+            uint32_t ph[4], pl[4];   // weights times value scales, as the second product takes them
+            {
+                const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+#pragma unroll
+                for (int j = 0; j < 2; ++j) {
+                    const float a = exp2_fast(s[j][0] - m0), b = exp2_fast(s[j][1] - m0);
+                    const float c = exp2_fast(s[j][2] - m1), d = exp2_fast(s[j][3] - m1);
+                    l[0] += a + b;
+                    l[1] += c + d;
+                    const float av = a * vs[2 * j], bv = b * vs[2 * j + 1], cv = c * vs[2 * j], dv = d * vs[2 * j + 1];
+                    ph[2 * j] = pack_f16x2(av, bv);
+                    ph[2 * j + 1] = pack_f16x2(cv, dv);
+                    if (F32) {
+                        pl[2 * j] = rest_f16x2(av, bv, ph[2 * j]);
+                        pl[2 * j + 1] = rest_f16x2(cv, dv, ph[2 * j + 1]);
+                    }
+                }
+            }
+            const uint32_t vb = base + S::CODES + t0 * D;
+            uint32_t va[4][DB / 4];   // codes of tokens a, b, 8 + a, 8 + b
+#pragma unroll
+            for (int k = 0; k < 4; ++k) {
+                const uint32_t a = vb + (k >> 1) * 8 * D + v_off[k & 1];
+                if constexpr (D == 128) {
+                    const uint4 x = lds128(a);
+                    va[k][0] = x.x; va[k][1] = x.y; va[k][2] = x.z; va[k][3] = x.w;
+                } else {
+                    const uint2 x = lds64(a);
+                    va[k][0] = x.x; va[k][1] = x.y;
+                }
+            }
+#pragma unroll
+            for (int c = 0; c < DB / 4; ++c) {
+#define SQ_PV(I)                                                                              \
+    {                                                                                         \
+        const uint32_t b0 = code_pair<I>(va[0][c], va[1][c]), b1 = code_pair<I>(va[2][c], va[3][c]); \
+        mma_f16(o[4 * c + I], ph, b0, b1);                                                    \
+        if (F32) mma_f16(o[4 * c + I], pl, b0, b1);                                           \
+    }
+                SQ_PV(0) SQ_PV(1) SQ_PV(2) SQ_PV(3)
+#undef SQ_PV
+            }
+        }
+        __syncwarp();
+        if (lane == 0) mbar_arrive(empty + 8 * st);
+
+        const bool ends = w.tile + 1 == w.nt;
+        if (ends || i + 1 == n_items) {   // the end of the piece: the warps' results meet
+            float2* at = meet[piece & 1][warp];
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
+                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
+                if (spoilt) l[r] = __int_as_float(0x7fc00000);
+                if (t4 == 0) at[gr + 8 * r] = make_float2(m[r], l[r]);
+            }
+            consumers_sync();
+#pragma unroll
+            for (int r = 0; r < 2; ++r) {
+                if (mt * 16 + gr + 8 * r >= R) continue;
+                float M = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + mt][gr + 8 * r].x);
+                const float f = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - M);
+                float* row = merge + (warp * 16 + gr + 8 * r) * S::ROW;
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    // channels DB (2 t4 + e) .. + DB - 1, behind a gap of 4 for each earlier t4
+                    float* dst = row + DB * (2 * t4 + e) + 4 * t4;
+#pragma unroll
+                    for (int n = 0; n < NT; n += 4)
+                        *reinterpret_cast<float4*>(dst + n) = make_float4(o[n][2 * r + e] * f, o[n + 1][2 * r + e] * f,
+                                                                          o[n + 2][2 * r + e] * f, o[n + 3][2 * r + e] * f);
+                }
+            }
+            consumers_sync();
+            const bool whole = ends && !began_before;
+            const int64_t slot = (2 * (int64_t)blockIdx.x + (began_before ? 0 : 1)) * (16 * MT);
+            for (int u = tid; u < R * (D / 4); u += 32 * kConsumers) {
+                const int row = u / (D / 4), d = u % (D / 4) * 4;
+                const int rm = row >> 4, rr = row & 15;
+                float M = -INFINITY, L = 0.0f;
+                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + rm][rr].x);
+#pragma unroll
+                for (int q = 0; q < TG; ++q) {
+                    const float2 ml = meet[piece & 1][q * MT + rm][rr];
+                    L += ml.x == -INFINITY ? ml.y : ml.y * exp2_fast(ml.x - M);   // ml.y is 0 there, or NaN
+                    const float4 x = *reinterpret_cast<const float4*>(merge + ((q * MT + rm) * 16 + rr) * S::ROW + d + 4 * (d / (2 * DB)));
+                    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                }
+                if (whole) {
+                    attn_result<T, D>(g, w.b, w.h, row, G, d, acc, M, L);
+                } else {
+                    if (d == 0) g.part_ml[slot + row] = make_float2(M, L);
+                    *reinterpret_cast<float4*>(g.part_o + (slot + row) * D + d) = acc;
+                }
+            }
+            ++piece;
+        }
+        if (i + 1 < n_items) w.next(g);
+        if (++st == S::STAGES) {
+            st = 0;
+            parity ^= 1u;
+        }
+    }
+}
+
+// Joins the partial results of the (sequence, head)s that several CTAs shared.
+// Block i - 1 looks at the border between the shares of CTAs i - 1 and i: if it
+// lies inside a (sequence, head) and is the first that does, this block's warps join
+// that one's rows, piece by piece in the CTAs' order.
+template <typename T, int D>
+__global__ void __launch_bounds__(128) kv_attention_join_kernel(const KvAttnArgs g, int n_ctas, int slot_rows) {
+    pdl_wait();
+    pdl_trigger();
+    const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
+    const int64_t W = *g.work;
+    auto border = [&](int c) { return W * c / n_ctas; };
+    const int64_t x = border(i);
+    if (x >= W) return;
+    const int4 at = g.start[i];
+    const int64_t begin = x - at.z, end = begin + at.w;
+    if (at.z == 0 || border(i - 1) > begin) return;
+    const int G = g.n_q_heads / g.c.n_heads;
+    const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
+    if (row >= G * g.q_len) return;
+    // CTAs i - 1 (slot 1) and i .. (slot 0) as far as their shares begin inside
+    int n = 1;
+    while (i - 1 + n < n_ctas && border(i - 1 + n) < end) ++n;
+    auto slot = [&](int p) { return (2 * (int64_t)(i - 1 + p) + (p == 0 ? 1 : 0)) * slot_rows + row; };
+    auto some = [&](int p) { return border(i - 1 + p) < border(i + p); };   // a share may be empty
+    float M = -INFINITY;
+    for (int p = lane; p < n; p += 32)
+        if (some(p)) M = fmaxf(M, g.part_ml[slot(p)].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
+    float L = 0.0f;
+    constexpr int E = D / 32;
+    float acc[E] = {};
+    for (int p = 0; p < n; ++p) {
+        if (!some(p)) continue;
+        const float2 ml = g.part_ml[slot(p)];
+        const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - M);
+        L += ml.x == -INFINITY ? ml.y : ml.y * f;
+        const float* o = g.part_o + slot(p) * D + lane * E;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] += o[e] * f;
+    }
+    const int qi = row / G, h = at.y * G + row % G;
+    const int64_t out_row = ((int64_t)at.x * g.q_len + qi) * g.n_q_heads + h;
+    const float inv = L == 0.0f ? 0.0f : 1.0f / L;
+#pragma unroll
+    for (int e = 0; e < E; ++e) put(static_cast<T*>(g.out) + out_row * D + lane * E + e, acc[e] * inv);
+    if (g.lse && lane == 0) g.lse[out_row] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
+}
+
+// Codes [pages * heads][page_size][D] as a map whose box is one page of one head, in the
+// swizzle whose rows are D bytes.
+sq_status make_map_pages(CUtensorMap* map, const void* base, int64_t slabs, int ps, int D) {
+    sq_status r = get_encoder();
+    if (r != SQ_OK) return r;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)ps, (cuuint64_t)slabs};
+    cuuint64_t strides[2] = {(cuuint64_t)D, (cuuint64_t)D * ps};
+    cuuint32_t box[3] = {(cuuint32_t)D, (cuuint32_t)ps, 1u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult cr = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B,
+                           CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (cr != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled failed (%d) for %lld pages", (int)cr, (long long)slabs);
+        return SQ_ERR_CUDA;
+    }
+    return SQ_OK;
+}
+
+int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+
+struct KvAttnLayout {
+    size_t start, ml, o, total;
+};
+KvAttnLayout kv_attn_layout(int ctas, int64_t rows, int D) {
+    const size_t slots = (size_t)ctas * 2 * 16 * row_tiles(rows);
+    KvAttnLayout L{};
+    L.start = 256;
+    L.ml = L.start + align256((size_t)ctas * sizeof(int4));
+    L.o = L.ml + align256(slots * sizeof(float2));
+    L.total = L.o + slots * D * sizeof(float);
+    return L;
+}
+
+template <typename T, int D, int MT>
+sq_status launch_kv_attention(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& g, cudaStream_t st) {
+    static bool attr_done[64] = {};
+    const DeviceInfo& di = device_info();
+    constexpr size_t smem = AttnSmem<D>::TOTAL;
+    sq_status r = ensure_smem_attr(kv_attention_kernel<T, D, MT>, smem, attr_done[di.device & 63]);
+    if (r != SQ_OK) return r;
+    r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, MT>, dim3(di.sm_count), dim3(kAttnThreads), smem, st, 1,
+                   mk, mv, g);
+    if (r != SQ_OK) return r;
+    const int rows = g.n_q_heads / g.c.n_heads * g.q_len;
+    return launch_pdl("kv_attention_join_kernel", kv_attention_join_kernel<T, D>, dim3(di.sm_count - 1, (rows + 3) / 4),
+                      dim3(128), 0, st, 1, g, di.sm_count, 16 * MT);
+}
+
+template <typename T, int D>
+sq_status launch_kv_attention_rows(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& g, cudaStream_t st) {
+    switch (row_tiles((int64_t)g.n_q_heads / g.c.n_heads * g.q_len)) {
+    case 1: return launch_kv_attention<T, D, 1>(mk, mv, g, st);
+    case 2: return launch_kv_attention<T, D, 2>(mk, mv, g, st);
+    case 4: return launch_kv_attention<T, D, 4>(mk, mv, g, st);
+    default: return launch_kv_attention<T, D, 8>(mk, mv, g, st);
+    }
 }
 
 sq_status kv_attention_impl(const void* q, int64_t q_stride, sq_dtype dt, const sq_kv_cache* cache,
@@ -83,7 +722,7 @@ sq_status kv_attention_impl(const void* q, int64_t q_stride, sq_dtype dt, const 
     if ((r = check_kv_dtype(dt)) != SQ_OK) return r;
     if ((r = check_cache(cache, block_table, max_pages, n_seqs, g.c)) != SQ_OK) return r;
     if (q_len < 0 || n_q_heads < 0) { set_error("negative size"); return SQ_ERR_INVALID_ARG; }
-    if (!(scale > -3.0e38f && scale < 3.0e38f)) { set_error("scale must be finite"); return SQ_ERR_INVALID_ARG; }
+    if (!(scale >= -1.0e38f && scale <= 1.0e38f)) { set_error("scale must be within +-1e38"); return SQ_ERR_INVALID_ARG; }
     if (n_q_heads % cache->n_heads != 0) {
         set_error("%lld query heads over %d heads of keys", (long long)n_q_heads, (int)cache->n_heads);
         return SQ_ERR_UNSUPPORTED;
@@ -97,16 +736,32 @@ sq_status kv_attention_impl(const void* q, int64_t q_stride, sq_dtype dt, const 
     if ((r = check_rows(q, q_stride, n_q_heads * D, dt == SQ_F32 ? 4 : 2, "q")) != SQ_OK) return r;
     if (!seq_len || !out) { set_error("seq_len or out: NULL pointer"); return SQ_ERR_INVALID_ARG; }
     if (!aligned16(out)) { set_error("out must be 16-byte aligned"); return SQ_ERR_UNSUPPORTED; }
-    (void)ws; (void)ws_bytes;
+    const int64_t rows = q_len * (n_q_heads / cache->n_heads);
+    const KvAttnLayout L = kv_attn_layout(device_info().sm_count, rows, D);
+    if (!ws || ws_bytes < L.total) {
+        set_error("workspace too small: %zu bytes given, %zu needed", ws_bytes, L.total);
+        return SQ_ERR_INVALID_ARG;
+    }
+    if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0) { set_error("workspace must be 256-byte aligned"); return SQ_ERR_UNSUPPORTED; }
     g.block_table = block_table; g.seq_len = seq_len; g.max_pages = max_pages; g.q_stride = q_stride;
     g.n_seqs = (int)n_seqs; g.q_len = (int)q_len; g.n_q_heads = (int)n_q_heads; g.scale = scale;
     g.q = q; g.out = out; g.lse = lse;
-    const dim3 grid((unsigned)((n_seqs * q_len * n_q_heads + 3) / 4)), block(128);
+    uint8_t* base = static_cast<uint8_t*>(ws);
+    g.wait_limit = wait_limit_cycles();
+    g.work = reinterpret_cast<int64_t*>(base);
+    g.start = reinterpret_cast<int4*>(base + L.start);
+    g.part_ml = reinterpret_cast<float2*>(base + L.ml);
+    g.part_o = reinterpret_cast<float*>(base + L.o);
+    // an empty cache has no page to map; any address serves, since no page number is valid
+    const int64_t slabs = cache->n_pages > 0 ? cache->n_pages * cache->n_heads : 1;
+    if (slabs > 2147483647LL) { set_error("cache too large"); return SQ_ERR_UNSUPPORTED; }
+    CUtensorMap mk, mv;
+    if ((r = make_map_pages(&mk, cache->n_pages > 0 ? cache->k : out, slabs, cache->page_size, D)) != SQ_OK) return r;
+    if ((r = make_map_pages(&mv, cache->n_pages > 0 ? cache->v : out, slabs, cache->page_size, D)) != SQ_OK) return r;
     if (dt == SQ_F32)
-        return D == 64 ? launch_pdl("kv_attention_kernel", kv_attention_kernel<float, 64>, grid, block, 0, st, 1, g)
-                       : launch_pdl("kv_attention_kernel", kv_attention_kernel<float, 128>, grid, block, 0, st, 1, g);
-    return D == 64 ? launch_pdl("kv_attention_kernel", kv_attention_kernel<__nv_bfloat16, 64>, grid, block, 0, st, 1, g)
-                   : launch_pdl("kv_attention_kernel", kv_attention_kernel<__nv_bfloat16, 128>, grid, block, 0, st, 1, g);
+        return D == 64 ? launch_kv_attention_rows<float, 64>(mk, mv, g, st) : launch_kv_attention_rows<float, 128>(mk, mv, g, st);
+    return D == 64 ? launch_kv_attention_rows<__nv_bfloat16, 64>(mk, mv, g, st)
+                   : launch_kv_attention_rows<__nv_bfloat16, 128>(mk, mv, g, st);
 }
 
 }  // namespace
@@ -115,8 +770,10 @@ sq_status kv_attention_impl(const void* q, int64_t q_stride, sq_dtype dt, const 
 extern "C" {
 
 size_t sq_kv_attention_workspace_size(const sq_kv_cache* cache, int64_t n_seqs, int64_t q_len, int64_t n_q_heads) {
-    (void)cache; (void)n_seqs; (void)q_len; (void)n_q_heads;
-    return 0;
+    if (!cache || n_seqs <= 0 || q_len <= 0 || n_q_heads <= 0 || cache->n_heads <= 0 || cache->head_dim <= 0) return 0;
+    const int64_t rows = q_len * (n_q_heads / cache->n_heads);
+    if (q_len > 128 || rows > 128) return 0;
+    return sq::kv_attn_layout(sq::device_info().sm_count, rows, cache->head_dim).total;
 }
 
 sq_status sq_kv_attention(const void* q, int64_t q_stride, sq_dtype dt, const sq_kv_cache* cache,
