@@ -41,10 +41,10 @@ struct KvAttnArgs {
 // ragged batch is balanced without the host knowing a length. A (sequence, head)
 // that several CTAs share leaves one partial result (reference, sum, accumulator) from
 // each in the workspace; a second small kernel joins them in a fixed order.
-//   Inside a CTA eight warps take 16 tokens of a tile each (with more than 16 rows, MT row
-// tiles times 8 / MT token groups), with a softmax reference, sum and accumulator
-// of their own that meet once at the end of a head's piece: no barrier
-// between warps inside the loop.
+//   Inside a CTA eight warps share the tiles in groups of 32 tokens (with more than 16
+// rows each group is taken once for each of MT row tiles); a warp keeps a softmax
+// reference, sum and accumulator of its own, and they meet once at the end of a
+// head's piece: no barrier between warps inside the loop.
 //   S = Q K^T and O += P V are m16n8k16 products with fp32 accumulators (rows
 // x tokens, rows x channels). The channels of a k step may come in any order as
 // long as Q and K agree, and the columns of S may be any tokens: the orders
@@ -52,21 +52,29 @@ struct KvAttnArgs {
 // without bank conflicts, and S's accumulators are P's operand registers as they lie.
 //   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
 //   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
-// w = 2^(s - m) vs, with the reference m at least the largest s + floor(log2 vs) less 8,
-// so that w stays inside fp16's normal range for scales of any size; the sum takes 2^(s - m).
-// References move only when a score is 2^8 above, which is rare after the first tiles.
+// w = 2^(s - m) vs goes to the second product, 2^(s - m) into the sum. The reference m is
+// moved only when some |w| is above 2^8 (rare after the first groups); then it
+// becomes the largest s + floor(log2 vs), so that w lies inside fp16's normal range
+// for scales of any size.
 constexpr int kTile = 128;
 constexpr int kConsumers = 8;
-constexpr int kAttnThreads = 32 * (kConsumers + 1);
-constexpr float kSlack = 8.0f;
-constexpr float kNoScale = -80.0f;   // exponent that stands for scales below 2^-80: 2^88 times 2^30 tokens is finite
+constexpr int kAttnThreads = 32 * (kConsumers + 4);   // and a warpgroup whose first warp loads
+// registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
+constexpr int kConsumerRegs = 224, kProducerRegs = 56;
+constexpr int kGroup = 32;                    // tokens of a warp's step
+constexpr int kGroups = kTile / kGroup;
+constexpr float kMaxWeight = 256.0f;
+constexpr float kNoReference = -1.0e30f;      // nothing seen yet: 2^(s - m) is infinite for any score, 0 for a masked one
+constexpr float kNoScale = -80.0f;            // exponent that stands for scales below 2^-80: 2^88 times 2^30 tokens is finite
 
-template <int D>
+// MT == 1: the queries of a piece travel with its first tile.
+template <typename T, int D, int MT>
 struct AttnSmem {
-    static constexpr int STAGES = D == 128 ? 4 : 6;
-    static constexpr int CODES = kTile * D;                   // bytes of K, and of V
-    static constexpr int STAGE = 2 * CODES + 2 * kTile * 4;   // and their scales
-    static constexpr int ROW = D + 16;                        // floats of a merge row: D with a gap of 4 in each quarter
+    static constexpr int STAGES = D == 128 ? (sizeof(T) == 4 ? 3 : 4) : 6;
+    static constexpr int CODES = kTile * D;                              // bytes of K, and of V
+    static constexpr int Q = 2 * CODES + 2 * kTile * 4;                  // behind the codes and their scales
+    static constexpr int STAGE = Q + (MT == 1 ? 16 * D * (int)sizeof(T) : 0);
+    static constexpr int ROW = D + 16;                                   // floats of a merge row: D with a gap of 4 in each quarter
     static constexpr int MERGE = kConsumers * 16 * ROW * 4;
     static constexpr int TOTAL = 1024 + STAGES * STAGE + MERGE;
 };
@@ -133,6 +141,9 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
 __device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
     asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
 }
+__device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
+}
 __device__ __forceinline__ void cp_async_arrive(uint32_t bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" :: "r"(bar) : "memory");
 }
@@ -177,7 +188,7 @@ __device__ __forceinline__ void attn_result(const KvAttnArgs& g, int b, int h, i
 template <typename T, int D, int MT>
 __global__ void __launch_bounds__(kAttnThreads, 1)
 kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs g) {
-    using S = AttnSmem<D>;
+    using S = AttnSmem<T, D, MT>;
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int KS = D / 16, NT = D / 8, DB = D / 8;   // k steps of S, column tiles of O, codes a lane holds of a value row
     constexpr int TG = kConsumers / MT;                  // token groups
@@ -195,7 +206,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
             mbar_init(full + 8 * i, 33);   // the producer's lanes (scales) and its expected bytes
-            mbar_init(empty + 8 * i, kConsumers);
+            mbar_init(empty + 8 * i, kGroups * MT);
         }
         abort_flag = 0;
         start_b = 0;
@@ -277,7 +288,9 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     const int64_t n_items = x1 - x0;
     const long long limit = g.wait_limit;
     volatile int* abort = &abort_flag;
-    if (warp == kConsumers) {
+    if (warp >= kConsumers) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kProducerRegs));
+        if (warp > kConsumers) return;
         // ---------------------------------------------------------------- producer
         const int ps = g.c.page_size, sh = g.c.page_shift, per = kTile >> sh;   // pages of a tile
         auto page_of = [&](const TileWalk& v) {   // lane i: page i of the tile, -2 if it holds no token
@@ -328,6 +341,15 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                     cp_async4(dst + 2 * S::CODES + kTile * 4 + t * 4, g.c.v_scale + at);
                 }
             }
+            if (MT == 1 && (i == 0 || w.tile == 0)) {   // a piece begins: its query rows
+                constexpr int PER = D * (int)sizeof(T) / 16;
+                for (int u = lane; u < R * PER; u += 32) {
+                    const int row = u / PER, c = u % PER;
+                    const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + row / G) * g.q_stride +
+                                 (int64_t)(w.h * G + row % G) * D;
+                    cp_async16(dst + S::Q + u * 16, reinterpret_cast<const uint8_t*>(q) + c * 16);
+                }
+            }
             cp_async_arrive(bar);
             ++issued;
             w = nx;
@@ -350,8 +372,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
 
     // -------------------------------------------------------------------- consumers
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kConsumerRegs));
     const int gr = lane >> 2, t4 = lane & 3;
-    const int mt = warp % MT, grp = warp / MT;
+    const int mt = warp % MT;
+    int next_group = warp / MT;   // groups are dealt to the warps of a row tile in turn
     const int pi_g = gr & 1 ? (gr + 4) & 7 : gr;          // the token of column gr: 0 5 2 7 4 1 6 3
     const int tok_a = 2 * t4, tok_b = (2 * t4 + 5) & 7;   // and of columns 2 t4, 2 t4 + 1
     uint32_t k_off[D / 64], v_off[2];
@@ -373,8 +397,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     int st = 0, piece = 0;
     uint32_t parity = 0;
     for (int64_t i = 0; i < n_items; ++i) {
-        if (i == 0 || w.tile == 0) {   // a new piece: its queries
-            spoilt = false;
+        const uint32_t base = ring + st * S::STAGE;
+        const bool begins = i == 0 || w.tile == 0;
+        if (begins || next_group < kGroups) {
+            mbar_wait(full + 8 * st, parity, limit, abort, SITE_KV_ATTENTION_WAIT);
+            if (stage_bad[st]) spoilt = true;
+        }
+        if (begins) {   // a new piece: its queries
+            spoilt = stage_bad[st] != 0;
             began_before = w.tile > 0;
             see_all = w.len - g.q_len + 1;
 #pragma unroll
@@ -383,13 +413,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
-                m[r] = -INFINITY;
+                m[r] = kNoReference;
                 l[r] = 0.0f;
                 const int row = mt * 16 + gr + 8 * r;
                 const bool has = row < R;
                 const int qi = has ? row / G : 0, hq = w.h * G + (has ? row % G : 0);
                 see[r] = has ? max(0, w.len - g.q_len + 1 + qi) : 0;
                 const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + qi) * g.q_stride + (int64_t)hq * D;
+                const T* qr = MT == 1 ? reinterpret_cast<const T*>(smem_raw + (base - smem_u32(smem_raw)) + S::Q) + (has ? row : 0) * D : q;
                 float x[KS][4];
                 float top = 0.0f;
 #pragma unroll
@@ -397,7 +428,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         float v[8];
-                        Chunk<T>::load(q + 64 * c + 16 * t4 + 8 * half, v);
+                        Chunk<T>::load(qr + 64 * c + 16 * t4 + 8 * half, v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             x[4 * c + 2 * half + (e >> 2)][e & 3] = v[e];
@@ -407,12 +438,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 }
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
                 top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-                const int ex = top > 0.0f ? ilogbf(top) : 0;   // |q| 2^-ex < 2
-                qs[r] = scalbnf(g.scale * 1.4426950408889634f, ex);
+                // a power of two that brings the row's largest value to 1 .. 4 (a subnormal one below 1)
+                const int ex = min(126, max(-126, (int)(__float_as_uint(top) >> 23) - 127));
+                const float down = __int_as_float((127 - ex) << 23);
+                qs[r] = g.scale * 1.4426950408889634f * __int_as_float((127 + ex) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) x[ks][e] = scalbnf(x[ks][e], -ex);
+                    for (int e = 0; e < 4; ++e) x[ks][e] *= down;
                     // codes 0 and 2 of a word make the first pair of a k step, 1 and 3 the second
                     qh[ks][r] = pack_f16x2(x[ks][0], x[ks][2]);
                     qh[ks][2 + r] = pack_f16x2(x[ks][1], x[ks][3]);
@@ -423,124 +456,134 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 }
             }
         }
-        mbar_wait(full + 8 * st, parity, limit, abort, SITE_KV_ATTENTION_WAIT);
-        const uint32_t base = ring + st * S::STAGE;
-        if (stage_bad[st]) spoilt = true;
 #pragma unroll 1
-        for (int sub = 0; sub < MT; ++sub) {
-            const int t0 = (grp + TG * sub) * 16;          // first of the 16 tokens, in the tile
+        for (; next_group < kGroups; next_group += TG) {
+            const int t0 = next_group * kGroup;            // first of the 32 tokens, in the tile
             const int p0 = w.tile * kTile + t0;            // and in the sequence
-            if (p0 >= w.len) break;
-            float s[2][4];
+            if (p0 < w.len) {
+                float s[4][4];
 #pragma unroll
-            for (int j = 0; j < 2; ++j) {
-                s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+                for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
-                    const uint4 kw = lds128(base + (t0 + 8 * j) * D + k_off[c]);
-                    const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        uint32_t b0, b1;
-                        codes_even_odd(ws[e], b0, b1);
-                        mma_f16(s[j], qh[4 * c + e], b0, b1);
-                        if (F32) mma_f16(s[j], ql[F32 ? 4 * c + e : 0], b0, b1);
-                    }
-                }
-            }
-            float vs[4], ve[4];   // the four tokens' value scales and their exponents
+                    for (int j = 0; j < 4; ++j) {
+                        const uint4 kw = lds128(base + (t0 + 8 * j) * D + k_off[c]);
+                        const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
 #pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    const uint32_t a = base + 2 * S::CODES + (t0 + 8 * j + (e ? tok_b : tok_a)) * 4;
-                    const float ks = lds32(a);
-                    const float v = lds32(a + kTile * 4);
-                    vs[2 * j + e] = v;
-                    ve[2 * j + e] = fmaxf((float)((int)(__float_as_uint(v) >> 23) - 127), kNoScale);
-                    s[j][e] *= qs[0] * ks;
-                    s[j][2 + e] *= qs[1] * ks;
-                }
-            if (p0 + 16 > see_all) {   // the end of what some row sees
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const int p = p0 + 8 * j + (e ? tok_b : tok_a);
-                        if (p >= see[0]) s[j][e] = -INFINITY;
-                        if (p >= see[1]) s[j][2 + e] = -INFINITY;
-                        if (p >= w.len) {   // its scales were not loaded
-                            vs[2 * j + e] = 0.0f;
-                            ve[2 * j + e] = kNoScale;
+                        for (int e = 0; e < 4; ++e) {
+                            uint32_t b0, b1;
+                            codes_even_odd(ws[e], b0, b1);
+                            mma_f16(s[j], qh[4 * c + e], b0, b1);
+                            if (F32) mma_f16(s[j], ql[F32 ? 4 * c + e : 0], b0, b1);
                         }
                     }
-            }
-            float top[2];
+                }
+                // scores in units of log2, by their keys' scales; the value scales
+                float vs[8];
 #pragma unroll
-            for (int r = 0; r < 2; ++r)
-                top[r] = fmaxf(fmaxf(s[0][2 * r] + ve[0], s[0][2 * r + 1] + ve[1]), fmaxf(s[1][2 * r] + ve[2], s[1][2 * r + 1] + ve[3]));
-            if (__any_sync(0xffffffffu, top[0] > m[0] + kSlack || top[1] > m[1] + kSlack)) {
+                for (int j = 0; j < 4; ++j)
 #pragma unroll
-                for (int r = 0; r < 2; ++r) {
-                    float x = top[r];
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                    x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                    x = fmaxf(x, m[r]);
-                    const float f = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - x);
-                    m[r] = x;
-                    l[r] *= f;
-#pragma unroll
-                    for (int n = 0; n < NT; ++n) {
-                        o[n][2 * r] *= f;
-                        o[n][2 * r + 1] *= f;
+                    for (int e = 0; e < 2; ++e) {
+                        const uint32_t a = base + 2 * S::CODES + (t0 + 8 * j + (e ? tok_b : tok_a)) * 4;
+                        const float ks = lds32(a);
+                        vs[2 * j + e] = lds32(a + kTile * 4);
+                        s[j][e] *= qs[0] * ks;
+                        s[j][2 + e] *= qs[1] * ks;
                     }
-                }
-            }
-            uint32_t ph[4], pl[4];   // weights times value scales, as the second product takes them
-            {
-                const float m0 = m[0] == -INFINITY ? 0.0f : m[0], m1 = m[1] == -INFINITY ? 0.0f : m[1];
+                if (p0 + kGroup > see_all) {   // the end of what some row sees
 #pragma unroll
-                for (int j = 0; j < 2; ++j) {
-                    const float a = exp2_fast(s[j][0] - m0), b = exp2_fast(s[j][1] - m0);
-                    const float c = exp2_fast(s[j][2] - m1), d = exp2_fast(s[j][3] - m1);
-                    l[0] += a + b;
-                    l[1] += c + d;
-                    const float av = a * vs[2 * j], bv = b * vs[2 * j + 1], cv = c * vs[2 * j], dv = d * vs[2 * j + 1];
-                    ph[2 * j] = pack_f16x2(av, bv);
-                    ph[2 * j + 1] = pack_f16x2(cv, dv);
-                    if (F32) {
-                        pl[2 * j] = rest_f16x2(av, bv, ph[2 * j]);
-                        pl[2 * j + 1] = rest_f16x2(cv, dv, ph[2 * j + 1]);
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int p = p0 + 8 * j + (e ? tok_b : tok_a);
+                            if (p >= see[0]) s[j][e] = -INFINITY;
+                            if (p >= see[1]) s[j][2 + e] = -INFINITY;
+                            if (p >= w.len) vs[2 * j + e] = 0.0f;   // its scales were not loaded
+                        }
+                }
+                float wt[4][4], sum[2];
+                auto weigh = [&](float& most) {
+                    most = 0.0f;
+                    sum[0] = sum[1] = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) {
+                            const float a = exp2_fast(s[j][e] - m[e >> 1]);
+                            sum[e >> 1] += a;
+                            wt[j][e] = a * vs[2 * j + (e & 1)];
+                            most = fmaxf(most, fabsf(wt[j][e]));
+                        }
+                };
+                float most;
+                weigh(most);
+                if (__any_sync(0xffffffffu, most > kMaxWeight)) {
+#pragma unroll
+                    for (int r = 0; r < 2; ++r) {
+                        float x = kNoReference;
+#pragma unroll
+                        for (int j = 0; j < 4; ++j)
+#pragma unroll
+                            for (int e = 0; e < 2; ++e) {
+                                const int ex = (int)((__float_as_uint(vs[2 * j + e]) >> 23) & 255u) - 127;
+                                x = fmaxf(x, s[j][2 * r + e] + fmaxf((float)ex, kNoScale));
+                            }
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+                        x = fmaxf(x, m[r]);
+                        const float f = exp2_fast(m[r] - x);
+                        m[r] = x;
+                        l[r] *= f;
+#pragma unroll
+                        for (int n = 0; n < NT; ++n) {
+                            o[n][2 * r] *= f;
+                            o[n][2 * r + 1] *= f;
+                        }
                     }
+                    weigh(most);
                 }
-            }
-            const uint32_t vb = base + S::CODES + t0 * D;
-            uint32_t va[4][DB / 4];   // codes of tokens a, b, 8 + a, 8 + b
+                l[0] += sum[0];
+                l[1] += sum[1];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) {
-                const uint32_t a = vb + (k >> 1) * 8 * D + v_off[k & 1];
-                if constexpr (D == 128) {
-                    const uint4 x = lds128(a);
-                    va[k][0] = x.x; va[k][1] = x.y; va[k][2] = x.z; va[k][3] = x.w;
-                } else {
-                    const uint2 x = lds64(a);
-                    va[k][0] = x.x; va[k][1] = x.y;
-                }
-            }
+                for (int half = 0; half < 2; ++half) {   // 16 tokens a k step
+                    uint32_t ph[4], pl[4];
 #pragma unroll
-            for (int c = 0; c < DB / 4; ++c) {
-#define SQ_PV(I)                                                                              \
-    {                                                                                         \
-        const uint32_t b0 = code_pair<I>(va[0][c], va[1][c]), b1 = code_pair<I>(va[2][c], va[3][c]); \
-        mma_f16(o[4 * c + I], ph, b0, b1);                                                    \
-        if (F32) mma_f16(o[4 * c + I], pl, b0, b1);                                           \
+                    for (int k = 0; k < 4; ++k) {
+                        const float* x = wt[2 * half + (k >> 1)] + 2 * (k & 1);
+                        ph[k] = pack_f16x2(x[0], x[1]);
+                        if (F32) pl[k] = rest_f16x2(x[0], x[1], ph[k]);
+                    }
+                    const uint32_t vb = base + S::CODES + (t0 + 16 * half) * D;
+                    uint32_t va[4][DB / 4];   // codes of tokens a, b, 8 + a, 8 + b
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a = vb + (k >> 1) * 8 * D + v_off[k & 1];
+                        if constexpr (D == 128) {
+                            const uint4 x = lds128(a);
+                            va[k][0] = x.x; va[k][1] = x.y; va[k][2] = x.z; va[k][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(a);
+                            va[k][0] = x.x; va[k][1] = x.y;
+                        }
+                    }
+#pragma unroll
+                    for (int c = 0; c < DB / 4; ++c) {
+#define SQ_PV(I)                                                                                             \
+    {                                                                                                        \
+        const uint32_t b0 = code_pair<I>(va[0][c], va[1][c]), b1 = code_pair<I>(va[2][c], va[3][c]);         \
+        mma_f16(o[4 * c + I], ph, b0, b1);                                                                   \
+        if (F32) mma_f16(o[4 * c + I], pl, b0, b1);                                                          \
     }
-                SQ_PV(0) SQ_PV(1) SQ_PV(2) SQ_PV(3)
+                        SQ_PV(0) SQ_PV(1) SQ_PV(2) SQ_PV(3)
 #undef SQ_PV
+                    }
+                }
             }
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * st);
         }
-        __syncwarp();
-        if (lane == 0) mbar_arrive(empty + 8 * st);
+        next_group -= kGroups;
 
         const bool ends = w.tile + 1 == w.nt;
         if (ends || i + 1 == n_items) {   // the end of the piece: the warps' results meet
@@ -556,10 +599,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
             for (int r = 0; r < 2; ++r) {
                 if (mt * 16 + gr + 8 * r >= R) continue;
-                float M = -INFINITY;
+                float M = kNoReference;
 #pragma unroll
                 for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + mt][gr + 8 * r].x);
-                const float f = m[r] == -INFINITY ? 0.0f : exp2_fast(m[r] - M);
+                const float f = exp2_fast(m[r] - M);
                 float* row = merge + (warp * 16 + gr + 8 * r) * S::ROW;
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
@@ -577,14 +620,14 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             for (int u = tid; u < R * (D / 4); u += 32 * kConsumers) {
                 const int row = u / (D / 4), d = u % (D / 4) * 4;
                 const int rm = row >> 4, rr = row & 15;
-                float M = -INFINITY, L = 0.0f;
+                float M = kNoReference, L = 0.0f;
                 float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
 #pragma unroll
                 for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + rm][rr].x);
 #pragma unroll
                 for (int q = 0; q < TG; ++q) {
                     const float2 ml = meet[piece & 1][q * MT + rm][rr];
-                    L += ml.x == -INFINITY ? ml.y : ml.y * exp2_fast(ml.x - M);   // ml.y is 0 there, or NaN
+                    L += ml.y * exp2_fast(ml.x - M);
                     const float4 x = *reinterpret_cast<const float4*>(merge + ((q * MT + rm) * 16 + rr) * S::ROW + d + 4 * (d / (2 * DB)));
                     acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
                 }
@@ -629,7 +672,7 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const KvAttnArgs
     while (i - 1 + n < n_ctas && border(i - 1 + n) < end) ++n;
     auto slot = [&](int p) { return (2 * (int64_t)(i - 1 + p) + (p == 0 ? 1 : 0)) * slot_rows + row; };
     auto some = [&](int p) { return border(i - 1 + p) < border(i + p); };   // a share may be empty
-    float M = -INFINITY;
+    float M = kNoReference;
     for (int p = lane; p < n; p += 32)
         if (some(p)) M = fmaxf(M, g.part_ml[slot(p)].x);
 #pragma unroll
@@ -640,8 +683,8 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const KvAttnArgs
     for (int p = 0; p < n; ++p) {
         if (!some(p)) continue;
         const float2 ml = g.part_ml[slot(p)];
-        const float f = ml.x == -INFINITY ? 0.0f : exp2_fast(ml.x - M);
-        L += ml.x == -INFINITY ? ml.y : ml.y * f;
+        const float f = exp2_fast(ml.x - M);
+        L += ml.y * f;
         const float* o = g.part_o + slot(p) * D + lane * E;
 #pragma unroll
         for (int e = 0; e < E; ++e) acc[e] += o[e] * f;
@@ -692,7 +735,7 @@ template <typename T, int D, int MT>
 sq_status launch_kv_attention(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& g, cudaStream_t st) {
     static bool attr_done[64] = {};
     const DeviceInfo& di = device_info();
-    constexpr size_t smem = AttnSmem<D>::TOTAL;
+    constexpr size_t smem = AttnSmem<T, D, MT>::TOTAL;
     sq_status r = ensure_smem_attr(kv_attention_kernel<T, D, MT>, smem, attr_done[di.device & 63]);
     if (r != SQ_OK) return r;
     r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, MT>, dim3(di.sm_count), dim3(kAttnThreads), smem, st, 1,
