@@ -26,8 +26,8 @@ struct KvAttnArgs {
     void* out;
     float* lse;
     long long wait_limit;
-    int64_t* work;      // in the workspace: the number of tiles,
-    int4* start;        // where each CTA begins (sequence, head, tile, tiles of the sequence),
+    int64_t* border;    // in the workspace: where each CTA's share begins, and the end of the last;
+    int4* start;        // what that tile is (sequence, head, tile, tiles of the sequence);
     float2* part_ml;    // and two partial results of each CTA
     float* part_o;
 };
@@ -58,7 +58,7 @@ struct KvAttnArgs {
 // for scales of any size.
 constexpr int kTile = 128;
 constexpr int kConsumers = 8;
-constexpr int kAttnThreads = 32 * (kConsumers + 4);   // and a warpgroup whose first warp loads
+constexpr int kAttnThreads = 32 * (kConsumers + 4);   // and a warpgroup whose first two warps load
 // registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
 constexpr int kConsumerRegs = 224, kProducerRegs = 56;
 constexpr int kGroup = 32;                    // tokens of a warp's step
@@ -99,7 +99,7 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t a, uint32_t b) {
     return sub_1152(lop_and_xor(__byte_perm(a, b, (4 + I) << 8 | I), 0x00ff00ffu, 0x64806480u));
 }
 __device__ __forceinline__ void mma_f16(float (&d)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
-    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
                  : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
                  : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
 }
@@ -194,7 +194,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     constexpr int TG = kConsumers / MT;                  // token groups
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * S::STAGES];
-    __shared__ int abort_flag, stage_bad[S::STAGES];
+    __shared__ int abort_flag, drain_flag, stage_bad[S::STAGES];
     __shared__ int64_t scan[kAttnThreads / 32 + 1];
     __shared__ int start_b;
     __shared__ int64_t start_prefix;
@@ -205,10 +205,11 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S::STAGES * S::STAGE);
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            mbar_init(full + 8 * i, 33);   // the producer's lanes (scales) and its expected bytes
+            mbar_init(full + 8 * i, 33);   // the scales' 32 lanes, and the codes' expected bytes
             mbar_init(empty + 8 * i, kGroups * MT);
         }
         abort_flag = 0;
+        drain_flag = 0;
         start_b = 0;
         start_prefix = 0;
         fence_barrier_init();
@@ -268,7 +269,8 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         w.tile = (int)((x0 - start_prefix) % w.nt);
     }
     if (tid == 0) {
-        if (blockIdx.x == 0) *g.work = W;
+        g.border[blockIdx.x] = x0;
+        if (blockIdx.x + 1 == gridDim.x) g.border[gridDim.x] = W;
         g.start[blockIdx.x] = make_int4(w.b, w.h, x0 < W ? w.tile : 0, w.nt);
     }
     const int G = g.n_q_heads / H, R = G * g.q_len;
@@ -290,81 +292,86 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     volatile int* abort = &abort_flag;
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kProducerRegs));
-        if (warp > kConsumers) return;
-        // ---------------------------------------------------------------- producer
+        if (warp > kConsumers + 1) return;
+        // ------------------------------------------------------------ producers
+        // The first warp sends the pages of codes, the second the scales and the
+        // queries: one warp's instructions for both took longer than a tile's
+        // transfer (2400 cycles a tile against 1400 at HBM's rate).
+        const bool sends_codes = warp == kConsumers;
         const int ps = g.c.page_size, sh = g.c.page_shift, per = kTile >> sh;   // pages of a tile
-        auto page_of = [&](const TileWalk& v) {   // lane i: page i of the tile, -2 if it holds no token
-            const int64_t p = (int64_t)v.tile * kTile + ((int64_t)lane << sh);
-            return lane < per && p < v.len ? __ldg(g.block_table + v.b * g.max_pages + (p >> sh)) : -2;
-        };
-        int page = n_items > 0 ? page_of(w) : -2;
-        int64_t issued = 0;
+        int held_b = -1, held_from = 0, held = 0;   // 32 entries of a sequence's block table, one a lane
         int st = 0;
         uint32_t parity = 0;
+        int64_t issued = 0;
         for (int64_t i = 0; i < n_items; ++i) {
-            TileWalk nx = w;
-            int next_page = -2;
-            if (i + 1 < n_items) {
-                nx.next(g);
-                next_page = page_of(nx);
+            const int from = w.tile * per;
+            if (w.b != held_b || from < held_from || from + per > held_from + 32) {
+                held_b = w.b;
+                held_from = from;
+                const int64_t e = from + lane;
+                held = (e << sh) < w.len ? __ldg(g.block_table + w.b * g.max_pages + e) : 0;
             }
             if (i >= S::STAGES) {
-                bool go = true;
-                if (lane == 0) go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
-                if (!__shfl_sync(0xffffffffu, go, 0)) break;
+                const bool go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
+                if (!__all_sync(0xffffffffu, go)) break;
             }
-            const bool there = page != -2;
-            const bool good = (uint32_t)page < (uint64_t)g.c.n_pages;
-            const unsigned bad = __ballot_sync(0xffffffffu, there && !good);
-            const unsigned load = __ballot_sync(0xffffffffu, there && good);
             const uint32_t dst = ring + st * S::STAGE;
             const uint32_t bar = full + 8 * st;
-            if (lane == 0) {
-                stage_bad[st] = bad != 0;
-                if (bad) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
-                mbar_arrive_expect_tx(bar, (uint32_t)__popc(load) * 2u * (uint32_t)(ps * D));
-            }
-            __syncwarp();
-            if (there && good) {
-                const int z = page * H + w.h;
-                tma_load_3d(dst + lane * ps * D, &map_k, bar, 0, 0, z);
-                tma_load_3d(dst + S::CODES + lane * ps * D, &map_v, bar, 0, 0, z);
-            }
             const int tokens = min(kTile, w.len - w.tile * kTile);
+            if (sends_codes) {
+                const int page = __shfl_sync(0xffffffffu, held, (from - held_from + lane) & 31);
+                const bool there = lane < per && (lane << sh) < tokens;
+                const bool good = there && (uint32_t)page < (uint64_t)g.c.n_pages;
+                const unsigned n_there = __popc(__ballot_sync(0xffffffffu, there)), n_good = __popc(__ballot_sync(0xffffffffu, good));
+                if (lane == 0) {
+                    stage_bad[st] = n_good != n_there;
+                    if (n_good != n_there) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
+                    mbar_arrive_expect_tx(bar, n_good * 2u * (uint32_t)(ps * D));
+                }
+                __syncwarp();
+                if (good) {
+                    const int z = page * H + w.h;
+                    tma_load_3d(dst + lane * ps * D, &map_k, bar, 0, 0, z);
+                    tma_load_3d(dst + S::CODES + lane * ps * D, &map_v, bar, 0, 0, z);
+                }
+            } else {
+                const int bs = g.c.block_shift;
 #pragma unroll
-            for (int k = 0; k < kTile / 32; ++k) {
-                const int t = k * 32 + lane;
-                const int pg = __shfl_sync(0xffffffffu, page, t >> sh);
-                if (t < tokens && (uint32_t)pg < (uint64_t)g.c.n_pages) {
-                    const int64_t at = (((int64_t)pg * H + w.h) << (sh - g.c.block_shift)) + ((t & (ps - 1)) >> g.c.block_shift);
-                    cp_async4(dst + 2 * S::CODES + t * 4, g.c.k_scale + at);
-                    cp_async4(dst + 2 * S::CODES + kTile * 4 + t * 4, g.c.v_scale + at);
+                for (int k = 0; k < kTile / 32; ++k) {
+                    const int t = k * 32 + lane;
+                    const int page = __shfl_sync(0xffffffffu, held, (from - held_from + (t >> sh)) & 31);
+                    if (t < tokens && (uint32_t)page < (uint64_t)g.c.n_pages) {
+                        const int64_t at = (((int64_t)page * H + w.h) << (sh - bs)) + ((t & (ps - 1)) >> bs);
+                        cp_async4(dst + 2 * S::CODES + t * 4, g.c.k_scale + at);
+                        cp_async4(dst + 2 * S::CODES + kTile * 4 + t * 4, g.c.v_scale + at);
+                    }
                 }
-            }
-            if (MT == 1 && (i == 0 || w.tile == 0)) {   // a piece begins: its query rows
-                constexpr int PER = D * (int)sizeof(T) / 16;
-                for (int u = lane; u < R * PER; u += 32) {
-                    const int row = u / PER, c = u % PER;
-                    const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + row / G) * g.q_stride +
-                                 (int64_t)(w.h * G + row % G) * D;
-                    cp_async16(dst + S::Q + u * 16, reinterpret_cast<const uint8_t*>(q) + c * 16);
+                if (MT == 1 && (i == 0 || w.tile == 0)) {   // a piece begins: its query rows
+                    constexpr int PER = D * (int)sizeof(T) / 16;
+                    for (int u = lane; u < R * PER; u += 32) {
+                        const int row = u / PER, c = u % PER;
+                        const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + row / G) * g.q_stride +
+                                     (int64_t)(w.h * G + row % G) * D;
+                        cp_async16(dst + S::Q + u * 16, reinterpret_cast<const uint8_t*>(q) + c * 16);
+                    }
                 }
+                cp_async_arrive(bar);
             }
-            cp_async_arrive(bar);
             ++issued;
-            w = nx;
-            page = next_page;
+            if (i + 1 < n_items) w.next(g);
             if (++st == S::STAGES) {
                 st = 0;
                 parity ^= 1u;
             }
         }
         if (*abort) {   // a wait ran out: the copies in flight end before the shared memory goes
-            __shared__ int drain;
-            if (lane == 0) {
-                drain = 0;
-                for (int64_t i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-                    mbar_wait(full + 8 * (int)(i % S::STAGES), (i / S::STAGES) & 1, limit, &drain, SITE_KV_ATTENTION_WAIT);
+            if (sends_codes) {
+                volatile int* drain = &drain_flag;
+                if (lane == 0)
+                    for (int64_t i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
+                        mbar_wait(full + 8 * (int)(i % S::STAGES), (i / S::STAGES) & 1, limit, drain, SITE_KV_ATTENTION_WAIT);
+            } else {
+                asm volatile("cp.async.wait_all;" ::: "memory");
             }
             __syncwarp();
         }
@@ -466,14 +473,15 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
 #pragma unroll
                 for (int c = 0; c < D / 64; ++c) {
+                    uint4 kw[4];
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) {
-                        const uint4 kw = lds128(base + (t0 + 8 * j) * D + k_off[c]);
-                        const uint32_t ws[4] = {kw.x, kw.y, kw.z, kw.w};
+                    for (int j = 0; j < 4; ++j) kw[j] = lds128(base + (t0 + 8 * j) * D + k_off[c]);
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) {
+                    for (int e = 0; e < 4; ++e) {   // four independent products in a row
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
                             uint32_t b0, b1;
-                            codes_even_odd(ws[e], b0, b1);
+                            codes_even_odd(e == 0 ? kw[j].x : e == 1 ? kw[j].y : e == 2 ? kw[j].z : kw[j].w, b0, b1);
                             mma_f16(s[j], qh[4 * c + e], b0, b1);
                             if (F32) mma_f16(s[j], ql[F32 ? 4 * c + e : 0], b0, b1);
                         }
@@ -501,6 +509,21 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                             if (p >= see[1]) s[j][2 + e] = -INFINITY;
                             if (p >= w.len) vs[2 * j + e] = 0.0f;   // its scales were not loaded
                         }
+                }
+                uint32_t va[2][4][DB / 4];   // values' codes: of tokens a, b, 8 + a, 8 + b of both k steps
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const uint32_t a = base + S::CODES + (t0 + 16 * half + 8 * (k >> 1)) * D + v_off[k & 1];
+                        if constexpr (D == 128) {
+                            const uint4 x = lds128(a);
+                            va[half][k][0] = x.x; va[half][k][1] = x.y; va[half][k][2] = x.z; va[half][k][3] = x.w;
+                        } else {
+                            const uint2 x = lds64(a);
+                            va[half][k][0] = x.x; va[half][k][1] = x.y;
+                        }
+                    }
                 }
                 float wt[4][4], sum[2];
                 auto weigh = [&](float& most) {
@@ -554,24 +577,12 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                         ph[k] = pack_f16x2(x[0], x[1]);
                         if (F32) pl[k] = rest_f16x2(x[0], x[1], ph[k]);
                     }
-                    const uint32_t vb = base + S::CODES + (t0 + 16 * half) * D;
-                    uint32_t va[4][DB / 4];   // codes of tokens a, b, 8 + a, 8 + b
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a = vb + (k >> 1) * 8 * D + v_off[k & 1];
-                        if constexpr (D == 128) {
-                            const uint4 x = lds128(a);
-                            va[k][0] = x.x; va[k][1] = x.y; va[k][2] = x.z; va[k][3] = x.w;
-                        } else {
-                            const uint2 x = lds64(a);
-                            va[k][0] = x.x; va[k][1] = x.y;
-                        }
-                    }
 #pragma unroll
                     for (int c = 0; c < DB / 4; ++c) {
 #define SQ_PV(I)                                                                                             \
     {                                                                                                        \
-        const uint32_t b0 = code_pair<I>(va[0][c], va[1][c]), b1 = code_pair<I>(va[2][c], va[3][c]);         \
+        const uint32_t b0 = code_pair<I>(va[half][0][c], va[half][1][c]),                              \
+                       b1 = code_pair<I>(va[half][2][c], va[half][3][c]);                              \
         mma_f16(o[4 * c + I], ph, b0, b1);                                                                   \
         if (F32) mma_f16(o[4 * c + I], pl, b0, b1);                                                          \
     }
@@ -651,43 +662,60 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 // Joins the partial results of the (sequence, head)s that several CTAs shared.
 // Block i - 1 looks at the border between the shares of CTAs i - 1 and i: if it
 // lies inside a (sequence, head) and is the first that does, this block's warps join
-// that one's rows, piece by piece in the CTAs' order.
+// that one's rows. A lane holds the reference and sum of one piece (32 at a time); the
+// accumulators are added in the CTAs' order.
 template <typename T, int D>
 __global__ void __launch_bounds__(128) kv_attention_join_kernel(const KvAttnArgs g, int n_ctas, int slot_rows) {
     pdl_wait();
     pdl_trigger();
     const int i = blockIdx.x + 1, lane = threadIdx.x & 31;
-    const int64_t W = *g.work;
-    auto border = [&](int c) { return W * c / n_ctas; };
-    const int64_t x = border(i);
-    if (x >= W) return;
+    const int64_t x = __ldg(g.border + i), x_before = __ldg(g.border + i - 1);
     const int4 at = g.start[i];
     const int64_t begin = x - at.z, end = begin + at.w;
-    if (at.z == 0 || border(i - 1) > begin) return;
+    if (at.z == 0 || x_before > begin) return;
     const int G = g.n_q_heads / g.c.n_heads;
     const int row = blockIdx.y * 4 + (threadIdx.x >> 5);
     if (row >= G * g.q_len) return;
-    // CTAs i - 1 (slot 1) and i .. (slot 0) as far as their shares begin inside
-    int n = 1;
-    while (i - 1 + n < n_ctas && border(i - 1 + n) < end) ++n;
-    auto slot = [&](int p) { return (2 * (int64_t)(i - 1 + p) + (p == 0 ? 1 : 0)) * slot_rows + row; };
-    auto some = [&](int p) { return border(i - 1 + p) < border(i + p); };   // a share may be empty
-    float M = kNoReference;
-    for (int p = lane; p < n; p += 32)
-        if (some(p)) M = fmaxf(M, g.part_ml[slot(p)].x);
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, o));
-    float L = 0.0f;
     constexpr int E = D / 32;
+    float M = kNoReference, L = 0.0f;
     float acc[E] = {};
-    for (int p = 0; p < n; ++p) {
-        if (!some(p)) continue;
-        const float2 ml = g.part_ml[slot(p)];
-        const float f = exp2_fast(ml.x - M);
-        L += ml.y * f;
-        const float* o = g.part_o + slot(p) * D + lane * E;
+    for (int p0 = 0;; p0 += 32) {   // pieces: CTA i - 1 (its slot 1), then i, i + 1, .. (slot 0) that begin inside
+        const int c = i - 1 + p0 + lane;
+        const bool in = c < n_ctas && __ldg(g.border + min(c, n_ctas)) < end;
+        const unsigned inside = __ballot_sync(0xffffffffu, in);
+        if (inside == 0) break;
+        const bool some = in && __ldg(g.border + c) < __ldg(g.border + c + 1);   // a share may be empty
+        const int64_t slot = (2 * (int64_t)c + (c == i - 1 ? 1 : 0)) * slot_rows + row;
+        const float2 ml = some ? g.part_ml[slot] : make_float2(kNoReference, 0.0f);
+        float m = ml.x;
 #pragma unroll
-        for (int e = 0; e < E; ++e) acc[e] += o[e] * f;
+        for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+        m = fmaxf(m, M);
+        const float old = exp2_fast(M - m), f = exp2_fast(ml.x - m);
+        float l = ml.y * f;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+        M = m;
+        L = L * old + l;
+#pragma unroll
+        for (int e = 0; e < E; ++e) acc[e] *= old;
+        const unsigned have = __ballot_sync(0xffffffffu, some);
+        const int n = 32 - __clz(inside);
+#pragma unroll 4
+        for (int p = 0; p < n; ++p) {
+            const float fp = __shfl_sync(0xffffffffu, f, p);
+            if (!((have >> p) & 1u)) continue;
+            const int cp = i - 1 + p0 + p;
+            const float* o = g.part_o + ((2 * (int64_t)cp + (cp == i - 1 ? 1 : 0)) * slot_rows + row) * D + lane * E;
+            if constexpr (E == 4) {
+                const float4 v = *reinterpret_cast<const float4*>(o);
+                acc[0] += v.x * fp; acc[1] += v.y * fp; acc[2] += v.z * fp; acc[3] += v.w * fp;
+            } else {
+                const float2 v = *reinterpret_cast<const float2*>(o);
+                acc[0] += v.x * fp; acc[1] += v.y * fp;
+            }
+        }
+        if (inside != 0xffffffffu) break;
     }
     const int qi = row / G, h = at.y * G + row % G;
     const int64_t out_row = ((int64_t)at.x * g.q_len + qi) * g.n_q_heads + h;
@@ -724,7 +752,7 @@ struct KvAttnLayout {
 KvAttnLayout kv_attn_layout(int ctas, int64_t rows, int D) {
     const size_t slots = (size_t)ctas * 2 * 16 * row_tiles(rows);
     KvAttnLayout L{};
-    L.start = 256;
+    L.start = align256((size_t)(ctas + 1) * sizeof(int64_t));
     L.ml = L.start + align256((size_t)ctas * sizeof(int4));
     L.o = L.ml + align256(slots * sizeof(float2));
     L.total = L.o + slots * D * sizeof(float);
@@ -791,7 +819,7 @@ sq_status kv_attention_impl(const void* q, int64_t q_stride, sq_dtype dt, const 
     g.q = q; g.out = out; g.lse = lse;
     uint8_t* base = static_cast<uint8_t*>(ws);
     g.wait_limit = wait_limit_cycles();
-    g.work = reinterpret_cast<int64_t*>(base);
+    g.border = reinterpret_cast<int64_t*>(base);
     g.start = reinterpret_cast<int4*>(base + L.start);
     g.part_ml = reinterpret_cast<float2*>(base + L.ml);
     g.part_o = reinterpret_cast<float*>(base + L.o);
