@@ -138,9 +138,6 @@ __device__ __forceinline__ void tma_load_3d(uint32_t dst, const void* tmap, uint
         " [%0], [%1, {%3, %4, %5}], [%2];"
         :: "r"(dst), "l"(tmap), "r"(bar), "r"(x), "r"(y), "r"(z) : "memory");
 }
-__device__ __forceinline__ void cp_async4(uint32_t dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" :: "r"(dst), "l"(src) : "memory");
-}
 __device__ __forceinline__ void cp_async16(uint32_t dst, const void* src) {
     asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" :: "r"(dst), "l"(src) : "memory");
 }
@@ -205,7 +202,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     float* merge = reinterpret_cast<float*>(smem_raw + (ring - smem_u32(smem_raw)) + S::STAGES * S::STAGE);
     if (tid == 0) {
         for (int i = 0; i < S::STAGES; ++i) {
-            mbar_init(full + 8 * i, 33);   // the scales' 32 lanes, and the codes' expected bytes
+            mbar_init(full + 8 * i, 65);   // the codes' expected bytes; a store and a copy of each lane of the scales' warp
             mbar_init(empty + 8 * i, kGroups * MT);
         }
         abort_flag = 0;
@@ -287,45 +284,51 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 g.lse[(int64_t)b * g.q_len * g.n_q_heads + i] = len < 0 ? v : -INFINITY;
     }
 
-    const int64_t n_items = x1 - x0;
+    const int n_items = (int)(x1 - x0);
     const long long limit = g.wait_limit;
     volatile int* abort = &abort_flag;
     if (warp >= kConsumers) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kProducerRegs));
         if (warp > kConsumers + 1) return;
         // ------------------------------------------------------------ producers
-        // The first warp sends the pages of codes, the second the scales and the
-        // queries: one warp's instructions for both took longer than a tile's
-        // transfer (2400 cycles a tile against 1400 at HBM's rate).
+        // The first warp sends the pages of codes by TMA, the second the scales, through
+        // registers: a lane has four tokens, whose scales are one load of 16, 8 or 4
+        // bytes (scale_block 1, 2, more), taken a tile ahead. (Scales sent by 4-byte
+        // asynchronous copies, one a token, cost that warp 1550 cycles a tile, which was
+        // the whole kernel's pace: 67 us for 128k tokens and 8 heads.)
         const bool sends_codes = warp == kConsumers;
-        const int ps = g.c.page_size, sh = g.c.page_shift, per = kTile >> sh;   // pages of a tile
+        const int ps = g.c.page_size, sh = g.c.page_shift, bs = g.c.block_shift, per = kTile >> sh;   // pages of a tile
         int held_b = -1, held_from = 0, held = 0;   // 32 entries of a sequence's block table, one a lane
         int st = 0;
         uint32_t parity = 0;
-        int64_t issued = 0;
-        for (int64_t i = 0; i < n_items; ++i) {
-            const int from = w.tile * per;
-            if (w.b != held_b || from < held_from || from + per > held_from + 32) {
-                held_b = w.b;
+        auto pages_of = [&](const TileWalk& v) {   // makes sure that a tile's entries are held; the place of the first
+            const int from = v.tile * per;
+            if (v.b != held_b || from < held_from || from + per > held_from + 32) {
+                held_b = v.b;
                 held_from = from;
-                const int64_t e = from + lane;
-                held = (e << sh) < w.len ? __ldg(g.block_table + w.b * g.max_pages + e) : 0;
+                const int64_t e = (int64_t)from + lane;
+                held = (e << sh) < v.len ? __ldg(g.block_table + v.b * g.max_pages + e) : 0;
             }
-            if (i >= S::STAGES) {
-                const bool go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
-                if (!__all_sync(0xffffffffu, go)) break;
-            }
-            const uint32_t dst = ring + st * S::STAGE;
-            const uint32_t bar = full + 8 * st;
-            const int tokens = min(kTile, w.len - w.tile * kTile);
-            if (sends_codes) {
-                const int page = __shfl_sync(0xffffffffu, held, (from - held_from + lane) & 31);
-                const bool there = lane < per && (lane << sh) < tokens;
+            return from - held_from;
+        };
+        int issued = 0;
+        if (sends_codes) {
+            for (int i = 0; i < n_items; ++i) {
+                const int at = pages_of(w);
+                if (i >= S::STAGES) {
+                    const bool go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
+                    if (!__all_sync(0xffffffffu, go)) break;
+                }
+                const uint32_t dst = ring + st * S::STAGE;
+                const uint32_t bar = full + 8 * st;
+                const int page = __shfl_sync(0xffffffffu, held, (at + lane) & 31);
+                const bool there = lane < per && (lane << sh) < w.len - w.tile * kTile;
                 const bool good = there && (uint32_t)page < (uint64_t)g.c.n_pages;
-                const unsigned n_there = __popc(__ballot_sync(0xffffffffu, there)), n_good = __popc(__ballot_sync(0xffffffffu, good));
+                const unsigned bad = __ballot_sync(0xffffffffu, there && !good);
+                const unsigned n_good = __popc(__ballot_sync(0xffffffffu, good));
                 if (lane == 0) {
-                    stage_bad[st] = n_good != n_there;
-                    if (n_good != n_there) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
+                    stage_bad[st] = bad != 0;
+                    if (bad) record_status(SQ_ERR_BOUNDS, SITE_KV_ATTENTION);
                     mbar_arrive_expect_tx(bar, n_good * 2u * (uint32_t)(ps * D));
                 }
                 __syncwarp();
@@ -334,42 +337,82 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                     tma_load_3d(dst + lane * ps * D, &map_k, bar, 0, 0, z);
                     tma_load_3d(dst + S::CODES + lane * ps * D, &map_v, bar, 0, 0, z);
                 }
-            } else {
-                const int bs = g.c.block_shift;
-#pragma unroll
-                for (int k = 0; k < kTile / 32; ++k) {
-                    const int t = k * 32 + lane;
-                    const int page = __shfl_sync(0xffffffffu, held, (from - held_from + (t >> sh)) & 31);
-                    if (t < tokens && (uint32_t)page < (uint64_t)g.c.n_pages) {
-                        const int64_t at = (((int64_t)page * H + w.h) << (sh - bs)) + ((t & (ps - 1)) >> bs);
-                        cp_async4(dst + 2 * S::CODES + t * 4, g.c.k_scale + at);
-                        cp_async4(dst + 2 * S::CODES + kTile * 4 + t * 4, g.c.v_scale + at);
+                ++issued;
+                if (i + 1 < n_items) w.next(g);
+                if (++st == S::STAGES) {
+                    st = 0;
+                    parity ^= 1u;
+                }
+            }
+        } else {
+            float4 ks = make_float4(0.0f, 0.0f, 0.0f, 0.0f), vs = ks;
+            auto take = [&](const TileWalk& v, float4& k, float4& x) {
+                const int at = pages_of(v);
+                const int t = 4 * lane;
+                const int page = __shfl_sync(0xffffffffu, held, (at + (t >> sh)) & 31);
+                if (t < v.len - v.tile * kTile && (uint32_t)page < (uint64_t)g.c.n_pages) {
+                    const int64_t a = (((int64_t)page * H + v.h) << (sh - bs)) + ((t & (ps - 1)) >> bs);
+                    if (bs == 0) {
+                        k = __ldg(reinterpret_cast<const float4*>(g.c.k_scale + a));
+                        x = __ldg(reinterpret_cast<const float4*>(g.c.v_scale + a));
+                    } else if (bs == 1) {
+                        const float2 p = __ldg(reinterpret_cast<const float2*>(g.c.k_scale + a));
+                        const float2 q = __ldg(reinterpret_cast<const float2*>(g.c.v_scale + a));
+                        k.x = p.x; k.y = p.y;
+                        x.x = q.x; x.y = q.y;
+                    } else {
+                        k.x = __ldg(g.c.k_scale + a);
+                        x.x = __ldg(g.c.v_scale + a);
                     }
                 }
+            };
+            // one value of each token from what was loaded; not before it is needed, for
+            // a use waits for the load
+            auto spread = [&](const float4& k) {
+                return bs == 0 ? k : bs == 1 ? make_float4(k.x, k.x, k.y, k.y) : make_float4(k.x, k.x, k.x, k.x);
+            };
+            if (n_items > 0) take(w, ks, vs);
+            for (int i = 0; i < n_items; ++i) {
+                TileWalk nx = w;
+                float4 nk = ks, nv = vs;
+                if (i + 1 < n_items) {
+                    nx.next(g);
+                    take(nx, nk, nv);
+                }
+                if (i >= S::STAGES) {
+                    const bool go = mbar_wait(empty + 8 * st, parity ^ 1u, limit, abort, SITE_KV_ATTENTION_WAIT);
+                    if (!__all_sync(0xffffffffu, go)) break;
+                }
+                const uint32_t bar = full + 8 * st;
+                uint8_t* stage = smem_raw + (ring - smem_u32(smem_raw)) + st * S::STAGE;
+                *reinterpret_cast<float4*>(stage + 2 * S::CODES + 16 * lane) = spread(ks);
+                *reinterpret_cast<float4*>(stage + 2 * S::CODES + kTile * 4 + 16 * lane) = spread(vs);
                 if (MT == 1 && (i == 0 || w.tile == 0)) {   // a piece begins: its query rows
                     constexpr int PER = D * (int)sizeof(T) / 16;
                     for (int u = lane; u < R * PER; u += 32) {
                         const int row = u / PER, c = u % PER;
                         const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + row / G) * g.q_stride +
                                      (int64_t)(w.h * G + row % G) * D;
-                        cp_async16(dst + S::Q + u * 16, reinterpret_cast<const uint8_t*>(q) + c * 16);
+                        cp_async16(smem_u32(stage) + S::Q + u * 16, reinterpret_cast<const uint8_t*>(q) + c * 16);
                     }
                 }
-                cp_async_arrive(bar);
-            }
-            ++issued;
-            if (i + 1 < n_items) w.next(g);
-            if (++st == S::STAGES) {
-                st = 0;
-                parity ^= 1u;
+                mbar_arrive(bar);       // the stores above
+                cp_async_arrive(bar);   // the copies above, when they are there
+                w = nx;
+                ks = nk;
+                vs = nv;
+                if (++st == S::STAGES) {
+                    st = 0;
+                    parity ^= 1u;
+                }
             }
         }
         if (*abort) {   // a wait ran out: the copies in flight end before the shared memory goes
             if (sends_codes) {
                 volatile int* drain = &drain_flag;
                 if (lane == 0)
-                    for (int64_t i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
-                        mbar_wait(full + 8 * (int)(i % S::STAGES), (i / S::STAGES) & 1, limit, drain, SITE_KV_ATTENTION_WAIT);
+                    for (int i = issued > S::STAGES ? issued - S::STAGES : 0; i < issued; ++i)
+                        mbar_wait(full + 8 * (i % S::STAGES), (i / S::STAGES) & 1, limit, drain, SITE_KV_ATTENTION_WAIT);
             } else {
                 asm volatile("cp.async.wait_all;" ::: "memory");
             }
@@ -403,7 +446,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     bool spoilt = false, began_before = false;
     int st = 0, piece = 0;
     uint32_t parity = 0;
-    for (int64_t i = 0; i < n_items; ++i) {
+    for (int i = 0; i < n_items; ++i) {
         const uint32_t base = ring + st * S::STAGE;
         const bool begins = i == 0 || w.tile == 0;
         if (begins || next_group < kGroups) {
@@ -525,6 +568,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                         }
                     }
                 }
+                // All of the group is in registers: its part of the stage is free
+                // before the weights and the second product, which are more than half of the step.
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * st);
                 float wt[4][4], sum[2];
                 auto weigh = [&](float& most) {
                     most = 0.0f;
@@ -590,9 +637,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #undef SQ_PV
                     }
                 }
+            } else {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * st);
             }
-            __syncwarp();
-            if (lane == 0) mbar_arrive(empty + 8 * st);
         }
         next_group -= kGroups;
 
