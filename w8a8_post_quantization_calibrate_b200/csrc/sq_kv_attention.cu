@@ -41,15 +41,16 @@ struct KvAttnArgs {
 // ragged batch is balanced without the host knowing a length. A (sequence, head)
 // that several CTAs share leaves one partial result (reference, sum, accumulator) from
 // each in the workspace; a second small kernel joins them in a fixed order.
-//   Inside a CTA eight warps share the tiles in groups of 32 tokens (with more than 16
+//   Inside a CTA the consumer warps take groups of 32 tokens in turn (with more than 16
 // rows each group is taken once for each of MT row tiles); a warp keeps a softmax
 // reference, sum and accumulator of its own, and they meet once at the end of a
 // head's piece: no barrier between warps inside the loop.
-//   S = Q K^T and O += P V are m16n8k16 products with fp32 accumulators (rows
-// x tokens, rows x channels). The channels of a k step may come in any order as
-// long as Q and K agree, and the columns of S may be any tokens: the orders
-// here are those in which one 16-byte shared-memory read gives a lane its codes
-// without bank conflicts, and S's accumulators are P's operand registers as they lie.
+//   S^T = K Q^T and O^T += V^T P^T are m16n8k16 products with fp32 accumulators: tokens
+// and channels make the 16 sides, rows the sides of 8, because R is often 8 or less. The
+// channels of a k step may come in any order as long as Q and K agree, and the rows of S^T
+// may be any tokens: the orders here are those in which one 16-byte shared-memory
+// read gives a lane its codes without bank conflicts. S^T's accumulators become P^T's
+// operand by an 8 x 8 transpose in registers.
 //   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
 //   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
 // w = 2^(s - m) vs goes to the second product, 2^(s - m) into the sum. The reference m is
@@ -57,26 +58,34 @@ struct KvAttnArgs {
 // becomes the largest s + floor(log2 vs), so that w lies inside fp16's normal range
 // for scales of any size.
 constexpr int kTile = 128;
-constexpr int kConsumers = 8;
-constexpr int kAttnThreads = 32 * (kConsumers + 4);   // and a warpgroup whose first two warps load
-// registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
-constexpr int kConsumerRegs = 224, kProducerRegs = 56;
+// Consumer warps: 12 for one side of 8 rows (152 registers each), 8 for two (224), so that
+// every accumulator stays in registers; and a warpgroup whose first two warps load.
+// 128 registers at launch times 16 warps are as many as 152 times 12 and 56 times 4;
+// 168 times 12 as many as 224 times 8 and 56 times 4.
+__host__ __device__ constexpr int consumer_warps(int NB) { return NB == 1 ? 12 : 8; }
+__host__ __device__ constexpr int attn_threads(int NB) { return 32 * (consumer_warps(NB) + 4); }
+__host__ __device__ constexpr int consumer_regs(int NB) { return NB == 1 ? 152 : 224; }
+constexpr int kProducerRegs = 56;
 constexpr int kGroup = 32;                    // tokens of a warp's step
 constexpr int kGroups = kTile / kGroup;
 constexpr float kMaxWeight = 256.0f;
 constexpr float kNoReference = -1.0e30f;      // nothing seen yet: 2^(s - m) is infinite for any score, 0 for a masked one
 constexpr float kNoScale = -80.0f;            // exponent that stands for scales below 2^-80: 2^88 times 2^30 tokens is finite
 
-// MT == 1: the queries of a piece travel with its first tile.
-template <typename T, int D, int MT>
+// NB sides of 8 rows a warp, MT row tiles. MT == 1: the queries of a piece travel with its first tile.
+template <typename T, int D, int NB, int MT>
 struct AttnSmem {
-    static constexpr int STAGES = D == 128 ? (sizeof(T) == 4 ? 3 : 4) : 6;
+    static constexpr int STAGES = D == 128 ? 4 : 6;
     static constexpr int CODES = kTile * D;                              // bytes of K, and of V
     static constexpr int Q = 2 * CODES + 2 * kTile * 4;                  // behind the codes and their scales
-    static constexpr int STAGE = Q + (MT == 1 ? 16 * D * (int)sizeof(T) : 0);
-    static constexpr int ROW = D + 16;                                   // floats of a merge row: D with a gap of 4 in each quarter
-    static constexpr int MERGE = kConsumers * 16 * ROW * 4;
+    static constexpr int STAGE = Q + (MT == 1 ? 8 * NB * D * (int)sizeof(T) : 0);
+    static constexpr int DB = D / 8;
+    static constexpr int ROW = D == 128 ? 164 : 100;                     // floats of a merge row: a gap of 4 behind every DB, and
+                                                                         // 4 mod 8, so that the 16-byte accesses meet no conflict
+    static constexpr int MERGE = consumer_warps(NB) * 8 * ROW * 4;
     static constexpr int TOTAL = 1024 + STAGES * STAGE + MERGE;
+    static_assert(STAGE % 1024 == 0, "a stage keeps the swizzle's alignment");
+    static_assert(TOTAL <= 227 * 1024 - 4096, "");
 };
 
 __device__ __forceinline__ uint32_t lop_and_xor(uint32_t x, uint32_t m, uint32_t c) {
@@ -167,7 +176,14 @@ struct TileWalk {
     }
 };
 
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kConsumers) : "memory"); }
+template <int THREADS>
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(THREADS) : "memory"); }
+// An 8 x 8 matrix of 16-bit values, two of a row in each lane, transposed.
+__device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
 
 // Four channels of a finished row.
 template <typename T, int D>
@@ -182,20 +198,21 @@ __device__ __forceinline__ void attn_result(const KvAttnArgs& g, int b, int h, i
     if (g.lse && d == 0) g.lse[at] = L == 0.0f ? -INFINITY : 0.6931471805599453f * (M + log2f(L));
 }
 
-template <typename T, int D, int MT>
-__global__ void __launch_bounds__(kAttnThreads, 1)
+template <typename T, int D, int NB, int MT>
+__global__ void __launch_bounds__(attn_threads(NB), 1)
 kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs g) {
-    using S = AttnSmem<T, D, MT>;
+    using S = AttnSmem<T, D, NB, MT>;
     constexpr bool F32 = sizeof(T) == 4;
-    constexpr int KS = D / 16, NT = D / 8, DB = D / 8;   // k steps of S, column tiles of O, codes a lane holds of a value row
-    constexpr int TG = kConsumers / MT;                  // token groups
+    constexpr int KS = D / 16, IT = D / 16, DB = D / 8;   // k steps of S, channel tiles of O, codes a lane holds of a value row
+    constexpr int kConsumers = consumer_warps(NB), kAttnThreads = attn_threads(NB);
+    constexpr int TG = kConsumers / MT;                   // warps of a row tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * S::STAGES];
     __shared__ int abort_flag, drain_flag, stage_bad[S::STAGES];
     __shared__ int64_t scan[kAttnThreads / 32 + 1];
     __shared__ int start_b;
     __shared__ int64_t start_prefix;
-    __shared__ float2 meet[2][kConsumers][16];
+    __shared__ float2 meet[2][kConsumers][8 * NB];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const uint32_t ring = (smem_u32(smem_raw) + 1023u) & ~1023u;
     const uint32_t full = smem_u32(bars), empty = full + 8 * S::STAGES;
@@ -422,12 +439,12 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
 
     // -------------------------------------------------------------------- consumers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kConsumerRegs));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(consumer_regs(NB)));
     const int gr = lane >> 2, t4 = lane & 3;
     const int mt = warp % MT;
     int next_group = warp / MT;   // groups are dealt to the warps of a row tile in turn
-    const int pi_g = gr & 1 ? (gr + 4) & 7 : gr;          // the token of column gr: 0 5 2 7 4 1 6 3
-    const int tok_a = 2 * t4, tok_b = (2 * t4 + 5) & 7;   // and of columns 2 t4, 2 t4 + 1
+    const int pi_g = gr & 1 ? (gr + 4) & 7 : gr;          // the token of row gr of an 8-row block: 0 5 2 7 4 1 6 3
+    const int tok_a = 2 * t4, tok_b = (2 * t4 + 5) & 7;   // and of rows 2 t4, 2 t4 + 1
     uint32_t k_off[D / 64], v_off[2];
     if (D == 128) {
         k_off[0] = pi_g * 128 + ((t4 ^ pi_g) << 4);
@@ -439,10 +456,12 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         v_off[0] = tok_a * 64 + ((((gr >> 1) ^ (tok_a >> 1)) << 4) | ((gr & 1) << 3));
         v_off[1] = tok_b * 64 + ((((gr >> 1) ^ (tok_b >> 1)) << 4) | ((gr & 1) << 3));
     }
-    uint32_t qh[KS][4], ql[F32 ? KS : 1][4];
-    float o[NT][4], m[2], l[2], qs[2];
-    int see[2];       // tokens that rows gr and gr + 8 see
-    int see_all = 0;  // and that every row of the tile sees
+    // Of each side of 8 rows: the queries as an operand (row gr); reference, sum, factor and
+    // tokens seen of rows 2 t4 and 2 t4 + 1, whose scores a lane holds.
+    uint32_t qh[NB][KS][2], ql[F32 ? NB : 1][F32 ? KS : 1][2];
+    float o[IT][NB][4], m[NB][2], l[NB][2], qs[NB][2];
+    int see[NB][2];
+    int see_all = 0;  // tokens that every row sees
     bool spoilt = false, began_before = false;
     int st = 0, piece = 0;
     uint32_t parity = 0;
@@ -458,19 +477,17 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
             began_before = w.tile > 0;
             see_all = w.len - g.q_len + 1;
 #pragma unroll
-            for (int n = 0; n < NT; ++n)
+            for (int n = 0; n < NB; ++n) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) o[n][e] = 0.0f;
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                m[r] = kNoReference;
-                l[r] = 0.0f;
-                const int row = mt * 16 + gr + 8 * r;
+                for (int k = 0; k < IT; ++k) o[k][n][0] = o[k][n][1] = o[k][n][2] = o[k][n][3] = 0.0f;
+                const int row = (mt * NB + n) * 8 + gr;
                 const bool has = row < R;
-                const int qi = has ? row / G : 0, hq = w.h * G + (has ? row % G : 0);
-                see[r] = has ? max(0, w.len - g.q_len + 1 + qi) : 0;
-                const T* q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + qi) * g.q_stride + (int64_t)hq * D;
-                const T* qr = MT == 1 ? reinterpret_cast<const T*>(smem_raw + (base - smem_u32(smem_raw)) + S::Q) + (has ? row : 0) * D : q;
+                const T* q;
+                if (MT == 1)
+                    q = reinterpret_cast<const T*>(smem_raw + (base - smem_u32(smem_raw)) + S::Q) + (has ? row : 0) * D;
+                else
+                    q = static_cast<const T*>(g.q) + ((int64_t)w.b * g.q_len + (has ? row / G : 0)) * g.q_stride +
+                        (int64_t)(w.h * G + (has ? row % G : 0)) * D;
                 float x[KS][4];
                 float top = 0.0f;
 #pragma unroll
@@ -478,7 +495,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
 #pragma unroll
                     for (int half = 0; half < 2; ++half) {
                         float v[8];
-                        Chunk<T>::load(qr + 64 * c + 16 * t4 + 8 * half, v);
+                        Chunk<T>::load(q + 64 * c + 16 * t4 + 8 * half, v);
 #pragma unroll
                         for (int e = 0; e < 8; ++e) {
                             x[4 * c + 2 * half + (e >> 2)][e & 3] = v[e];
@@ -491,18 +508,26 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 // a power of two that brings the row's largest value to 1 .. 4 (a subnormal one below 1)
                 const int ex = min(126, max(-126, (int)(__float_as_uint(top) >> 23) - 127));
                 const float down = __int_as_float((127 - ex) << 23);
-                qs[r] = g.scale * 1.4426950408889634f * __int_as_float((127 + ex) << 23);
+                const float up = g.scale * 1.4426950408889634f * __int_as_float((127 + ex) << 23);
 #pragma unroll
                 for (int ks = 0; ks < KS; ++ks) {
 #pragma unroll
                     for (int e = 0; e < 4; ++e) x[ks][e] *= down;
                     // codes 0 and 2 of a word make the first pair of a k step, 1 and 3 the second
-                    qh[ks][r] = pack_f16x2(x[ks][0], x[ks][2]);
-                    qh[ks][2 + r] = pack_f16x2(x[ks][1], x[ks][3]);
+                    qh[n][ks][0] = pack_f16x2(x[ks][0], x[ks][2]);
+                    qh[n][ks][1] = pack_f16x2(x[ks][1], x[ks][3]);
                     if (F32) {
-                        ql[F32 ? ks : 0][r] = rest_f16x2(x[ks][0], x[ks][2], qh[ks][r]);
-                        ql[F32 ? ks : 0][2 + r] = rest_f16x2(x[ks][1], x[ks][3], qh[ks][2 + r]);
+                        ql[F32 ? n : 0][F32 ? ks : 0][0] = rest_f16x2(x[ks][0], x[ks][2], qh[n][ks][0]);
+                        ql[F32 ? n : 0][F32 ? ks : 0][1] = rest_f16x2(x[ks][1], x[ks][3], qh[n][ks][1]);
                     }
+                }
+#pragma unroll
+                for (int e = 0; e < 2; ++e) {
+                    const int r = (mt * NB + n) * 8 + 2 * t4 + e;
+                    m[n][e] = kNoReference;
+                    l[n][e] = 0.0f;
+                    qs[n][e] = __shfl_sync(0xffffffffu, up, 4 * (2 * t4 + e));
+                    see[n][e] = r < R ? max(0, see_all + r / G) : 0;
                 }
             }
         }
@@ -510,192 +535,218 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
         for (; next_group < kGroups; next_group += TG) {
             const int t0 = next_group * kGroup;            // first of the 32 tokens, in the tile
             const int p0 = w.tile * kTile + t0;            // and in the sequence
-            if (p0 < w.len) {
-                float s[4][4];
+            if (p0 >= w.len) {
+                __syncwarp();
+                if (lane == 0) mbar_arrive(empty + 8 * st);
+                continue;
+            }
+            // j: blocks of 8 tokens; j / 2: the 16 tokens of a product
+            float s[2][NB][4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j) s[j][0] = s[j][1] = s[j][2] = s[j][3] = 0.0f;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
-                for (int c = 0; c < D / 64; ++c) {
-                    uint4 kw[4];
+                for (int e = 0; e < 4; ++e) s[0][n][e] = s[1][n][e] = 0.0f;
 #pragma unroll
-                    for (int j = 0; j < 4; ++j) kw[j] = lds128(base + (t0 + 8 * j) * D + k_off[c]);
+            for (int c = 0; c < D / 64; ++c) {
+                uint4 kw[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) {   // four independent products in a row
+                for (int j = 0; j < 4; ++j) kw[j] = lds128(base + (t0 + 8 * j) * D + k_off[c]);
 #pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            uint32_t b0, b1;
-                            codes_even_odd(e == 0 ? kw[j].x : e == 1 ? kw[j].y : e == 2 ? kw[j].z : kw[j].w, b0, b1);
-                            mma_f16(s[j], qh[4 * c + e], b0, b1);
-                            if (F32) mma_f16(s[j], ql[F32 ? 4 * c + e : 0], b0, b1);
+                for (int e = 0; e < 4; ++e)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        uint32_t a[4];
+                        codes_even_odd(e == 0 ? kw[2 * h].x : e == 1 ? kw[2 * h].y : e == 2 ? kw[2 * h].z : kw[2 * h].w, a[0], a[2]);
+                        codes_even_odd(e == 0 ? kw[2 * h + 1].x : e == 1 ? kw[2 * h + 1].y : e == 2 ? kw[2 * h + 1].z : kw[2 * h + 1].w,
+                                       a[1], a[3]);
+#pragma unroll
+                        for (int n = 0; n < NB; ++n) {
+                            mma_f16(s[h][n], a, qh[n][4 * c + e][0], qh[n][4 * c + e][1]);
+                            if (F32) mma_f16(s[h][n], a, ql[F32 ? n : 0][F32 ? 4 * c + e : 0][0], ql[F32 ? n : 0][F32 ? 4 * c + e : 0][1]);
                         }
                     }
-                }
-                // scores in units of log2, by their keys' scales; the value scales
-                float vs[8];
+            }
+            float vs[4];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
+            for (int j = 0; j < 4; ++j) {   // scores in units of log2, by their keys' scales; the value scales
+                const uint32_t a = base + 2 * S::CODES + (t0 + 8 * j + pi_g) * 4;
+                const float ks = lds32(a);
+                vs[j] = lds32(a + kTile * 4);
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        const uint32_t a = base + 2 * S::CODES + (t0 + 8 * j + (e ? tok_b : tok_a)) * 4;
-                        const float ks = lds32(a);
-                        vs[2 * j + e] = lds32(a + kTile * 4);
-                        s[j][e] *= qs[0] * ks;
-                        s[j][2 + e] *= qs[1] * ks;
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) s[j >> 1][n][2 * (j & 1) + e] *= qs[n][e] * ks;
+            }
+            uint32_t va[2][4][DB / 4];   // values' codes: of tokens a, b, 8 + a, 8 + b of both k steps
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+#pragma unroll
+                for (int k = 0; k < 4; ++k) {
+                    const uint32_t a = base + S::CODES + (t0 + 16 * half + 8 * (k >> 1)) * D + v_off[k & 1];
+                    if constexpr (D == 128) {
+                        const uint4 x = lds128(a);
+                        va[half][k][0] = x.x; va[half][k][1] = x.y; va[half][k][2] = x.z; va[half][k][3] = x.w;
+                    } else {
+                        const uint2 x = lds64(a);
+                        va[half][k][0] = x.x; va[half][k][1] = x.y;
                     }
-                if (p0 + kGroup > see_all) {   // the end of what some row sees
+                }
+            }
+            // All of the group is in registers: its part of the stage is free
+            // before the weights and the second product.
+            __syncwarp();
+            if (lane == 0) mbar_arrive(empty + 8 * st);
+            if (p0 + kGroup > see_all) {   // the end of what some row sees
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const int p = p0 + 8 * j + pi_g;
+#pragma unroll
+                    for (int n = 0; n < NB; ++n)
+#pragma unroll
+                        for (int e = 0; e < 2; ++e)
+                            if (p >= see[n][e]) s[j >> 1][n][2 * (j & 1) + e] = -INFINITY;
+                    if (p >= w.len) vs[j] = 0.0f;   // its scales were not loaded
+                }
+            }
+            float wt[2][NB][4], sum[NB][2];
+            auto weigh = [&](float& most) {
+                most = 0.0f;
+#pragma unroll
+                for (int n = 0; n < NB; ++n) {
+                    sum[n][0] = sum[n][1] = 0.0f;
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int p = p0 + 8 * j + (e ? tok_b : tok_a);
-                            if (p >= see[0]) s[j][e] = -INFINITY;
-                            if (p >= see[1]) s[j][2 + e] = -INFINITY;
-                            if (p >= w.len) vs[2 * j + e] = 0.0f;   // its scales were not loaded
+                            const float a = exp2_fast(s[j >> 1][n][2 * (j & 1) + e] - m[n][e]);
+                            sum[n][e] += a;
+                            wt[j >> 1][n][2 * (j & 1) + e] = a * vs[j];
+                            most = fmaxf(most, fabsf(a * vs[j]));
                         }
                 }
-                uint32_t va[2][4][DB / 4];   // values' codes: of tokens a, b, 8 + a, 8 + b of both k steps
+            };
+            float most;
+            weigh(most);
+            if (__any_sync(0xffffffffu, most > kMaxWeight)) {
+                float ex[4];
 #pragma unroll
-                for (int half = 0; half < 2; ++half) {
+                for (int j = 0; j < 4; ++j)
+                    ex[j] = fmaxf((float)((int)((__float_as_uint(vs[j]) >> 23) & 255u) - 127), kNoScale);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t a = base + S::CODES + (t0 + 16 * half + 8 * (k >> 1)) * D + v_off[k & 1];
-                        if constexpr (D == 128) {
-                            const uint4 x = lds128(a);
-                            va[half][k][0] = x.x; va[half][k][1] = x.y; va[half][k][2] = x.z; va[half][k][3] = x.w;
-                        } else {
-                            const uint2 x = lds64(a);
-                            va[half][k][0] = x.x; va[half][k][1] = x.y;
+                for (int n = 0; n < NB; ++n)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = m[n][e];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) x = fmaxf(x, s[j >> 1][n][2 * (j & 1) + e] + ex[j]);
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 4));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 8));
+                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 16));
+                        const float f = exp2_fast(m[n][e] - x);
+                        m[n][e] = x;
+                        l[n][e] *= f;
+#pragma unroll
+                        for (int k = 0; k < IT; ++k) {
+                            o[k][n][e] *= f;
+                            o[k][n][2 + e] *= f;
                         }
                     }
-                }
-                // All of the group is in registers: its part of the stage is free
-                // before the weights and the second product, which are more than half of the step.
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty + 8 * st);
-                float wt[4][4], sum[2];
-                auto weigh = [&](float& most) {
-                    most = 0.0f;
-                    sum[0] = sum[1] = 0.0f;
-#pragma unroll
-                    for (int j = 0; j < 4; ++j)
-#pragma unroll
-                        for (int e = 0; e < 4; ++e) {
-                            const float a = exp2_fast(s[j][e] - m[e >> 1]);
-                            sum[e >> 1] += a;
-                            wt[j][e] = a * vs[2 * j + (e & 1)];
-                            most = fmaxf(most, fabsf(wt[j][e]));
-                        }
-                };
-                float most;
                 weigh(most);
-                if (__any_sync(0xffffffffu, most > kMaxWeight)) {
+            }
 #pragma unroll
-                    for (int r = 0; r < 2; ++r) {
-                        float x = kNoReference;
+            for (int n = 0; n < NB; ++n) {
+                l[n][0] += sum[n][0];
+                l[n][1] += sum[n][1];
+            }
 #pragma unroll
-                        for (int j = 0; j < 4; ++j)
+            for (int half = 0; half < 2; ++half) {   // 16 tokens a k step
+                uint32_t ph[NB][2], pl[F32 ? NB : 1][2];
 #pragma unroll
-                            for (int e = 0; e < 2; ++e) {
-                                const int ex = (int)((__float_as_uint(vs[2 * j + e]) >> 23) & 255u) - 127;
-                                x = fmaxf(x, s[j][2 * r + e] + fmaxf((float)ex, kNoScale));
-                            }
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-                        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-                        x = fmaxf(x, m[r]);
-                        const float f = exp2_fast(m[r] - x);
-                        m[r] = x;
-                        l[r] *= f;
+                for (int n = 0; n < NB; ++n)
 #pragma unroll
-                        for (int n = 0; n < NT; ++n) {
-                            o[n][2 * r] *= f;
-                            o[n][2 * r + 1] *= f;
-                        }
-                    }
-                    weigh(most);
-                }
-                l[0] += sum[0];
-                l[1] += sum[1];
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {   // 16 tokens a k step
-                    uint32_t ph[4], pl[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float* x = wt[2 * half + (k >> 1)] + 2 * (k & 1);
-                        ph[k] = pack_f16x2(x[0], x[1]);
-                        if (F32) pl[k] = rest_f16x2(x[0], x[1], ph[k]);
+                    for (int k = 0; k < 2; ++k) {
+                        const float x = wt[half][n][2 * k], y = wt[half][n][2 * k + 1];
+                        const uint32_t hi = pack_f16x2(x, y);
+                        ph[n][k] = transpose_8x8(hi);
+                        if (F32) pl[F32 ? n : 0][k] = transpose_8x8(rest_f16x2(x, y, hi));
                     }
 #pragma unroll
-                    for (int c = 0; c < DB / 4; ++c) {
-#define SQ_PV(I)                                                                                             \
-    {                                                                                                        \
-        const uint32_t b0 = code_pair<I>(va[half][0][c], va[half][1][c]),                              \
-                       b1 = code_pair<I>(va[half][2][c], va[half][3][c]);                              \
-        mma_f16(o[4 * c + I], ph, b0, b1);                                                                   \
-        if (F32) mma_f16(o[4 * c + I], pl, b0, b1);                                                          \
+                for (int c = 0; c < DB / 4; ++c) {
+#define SQ_PV(I)                                                                                                 \
+    {                                                                                                            \
+        const uint32_t a[4] = {code_pair<2 * I>(va[half][0][c], va[half][1][c]),                                 \
+                               code_pair<2 * I + 1>(va[half][0][c], va[half][1][c]),                             \
+                               code_pair<2 * I>(va[half][2][c], va[half][3][c]),                                 \
+                               code_pair<2 * I + 1>(va[half][2][c], va[half][3][c])};                            \
+        _Pragma("unroll") for (int n = 0; n < NB; ++n) {                                                         \
+            mma_f16(o[2 * c + I][n], a, ph[n][0], ph[n][1]);                                                     \
+            if (F32) mma_f16(o[2 * c + I][n], a, pl[F32 ? n : 0][0], pl[F32 ? n : 0][1]);                        \
+        }                                                                                                        \
     }
-                        SQ_PV(0) SQ_PV(1) SQ_PV(2) SQ_PV(3)
+                    SQ_PV(0) SQ_PV(1)
 #undef SQ_PV
-                    }
                 }
-            } else {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(empty + 8 * st);
             }
         }
         next_group -= kGroups;
 
         const bool ends = w.tile + 1 == w.nt;
         if (ends || i + 1 == n_items) {   // the end of the piece: the warps' results meet
-            float2* at = meet[piece & 1][warp];
+            float2 (*all)[8 * NB] = meet[piece & 1];
 #pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 1);
-                l[r] += __shfl_xor_sync(0xffffffffu, l[r], 2);
-                if (spoilt) l[r] = __int_as_float(0x7fc00000);
-                if (t4 == 0) at[gr + 8 * r] = make_float2(m[r], l[r]);
-            }
-            consumers_sync();
-#pragma unroll
-            for (int r = 0; r < 2; ++r) {
-                if (mt * 16 + gr + 8 * r >= R) continue;
-                float M = kNoReference;
-#pragma unroll
-                for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + mt][gr + 8 * r].x);
-                const float f = exp2_fast(m[r] - M);
-                float* row = merge + (warp * 16 + gr + 8 * r) * S::ROW;
+            for (int n = 0; n < NB; ++n)
 #pragma unroll
                 for (int e = 0; e < 2; ++e) {
-                    // channels DB (2 t4 + e) .. + DB - 1, behind a gap of 4 for each earlier t4
-                    float* dst = row + DB * (2 * t4 + e) + 4 * t4;
-#pragma unroll
-                    for (int n = 0; n < NT; n += 4)
-                        *reinterpret_cast<float4*>(dst + n) = make_float4(o[n][2 * r + e] * f, o[n + 1][2 * r + e] * f,
-                                                                          o[n + 2][2 * r + e] * f, o[n + 3][2 * r + e] * f);
+                    float x = l[n][e];
+                    x += __shfl_xor_sync(0xffffffffu, x, 4);
+                    x += __shfl_xor_sync(0xffffffffu, x, 8);
+                    x += __shfl_xor_sync(0xffffffffu, x, 16);
+                    if (spoilt) x = __int_as_float(0x7fc00000);
+                    if (gr == 0) all[warp][n * 8 + 2 * t4 + e] = make_float2(m[n][e], x);
                 }
-            }
-            consumers_sync();
+            consumers_sync<32 * kConsumers>();
             const bool whole = ends && !began_before;
-            const int64_t slot = (2 * (int64_t)blockIdx.x + (began_before ? 0 : 1)) * (16 * MT);
-            for (int u = tid; u < R * (D / 4); u += 32 * kConsumers) {
-                const int row = u / (D / 4), d = u % (D / 4) * 4;
-                const int rm = row >> 4, rr = row & 15;
-                float M = kNoReference, L = 0.0f;
-                float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+            const int64_t slot = (2 * (int64_t)blockIdx.x + (began_before ? 0 : 1)) * (8 * NB * MT);
 #pragma unroll
-                for (int q = 0; q < TG; ++q) M = fmaxf(M, meet[piece & 1][q * MT + rm][rr].x);
+            for (int n = 0; n < NB; ++n) {   // 8 rows of each row tile at a time
 #pragma unroll
-                for (int q = 0; q < TG; ++q) {
-                    const float2 ml = meet[piece & 1][q * MT + rm][rr];
-                    L += ml.y * exp2_fast(ml.x - M);
-                    const float4 x = *reinterpret_cast<const float4*>(merge + ((q * MT + rm) * 16 + rr) * S::ROW + d + 4 * (d / (2 * DB)));
-                    acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                for (int e = 0; e < 2; ++e) {
+                    const int rr = 2 * t4 + e;
+                    if ((mt * NB + n) * 8 + rr >= R) continue;
+                    float M = kNoReference;
+#pragma unroll
+                    for (int q = 0; q < TG; ++q) M = fmaxf(M, all[q * MT + mt][n * 8 + rr].x);
+                    const float f = exp2_fast(m[n][e] - M);
+                    float* dst = merge + (warp * 8 + rr) * S::ROW + (DB + 4) * gr;   // channels DB gr .. + DB - 1
+#pragma unroll
+                    for (int k = 0; k < IT; k += 2)
+                        *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[k][n][e] * f, o[k][n][2 + e] * f,
+                                                                              o[k + 1][n][e] * f, o[k + 1][n][2 + e] * f);
                 }
-                if (whole) {
-                    attn_result<T, D>(g, w.b, w.h, row, G, d, acc, M, L);
-                } else {
-                    if (d == 0) g.part_ml[slot + row] = make_float2(M, L);
-                    *reinterpret_cast<float4*>(g.part_o + (slot + row) * D + d) = acc;
+                consumers_sync<32 * kConsumers>();
+                for (int u = tid; u < MT * 8 * (D / 4); u += 32 * kConsumers) {
+                    const int d = u % (D / 4) * 4, rr = u / (D / 4) % 8, rm = u / (2 * D);
+                    const int row = (rm * NB + n) * 8 + rr;
+                    if (row >= R) continue;
+                    float M = kNoReference, L = 0.0f;
+                    float4 acc = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll
+                    for (int q = 0; q < TG; ++q) M = fmaxf(M, all[q * MT + rm][n * 8 + rr].x);
+#pragma unroll
+                    for (int q = 0; q < TG; ++q) {
+                        const float2 ml = all[q * MT + rm][n * 8 + rr];
+                        L += ml.y * exp2_fast(ml.x - M);
+                        const float4 x = *reinterpret_cast<const float4*>(merge + ((q * MT + rm) * 8 + rr) * S::ROW + d + 4 * (d / DB));
+                        acc.x += x.x; acc.y += x.y; acc.z += x.z; acc.w += x.w;
+                    }
+                    if (whole) {
+                        attn_result<T, D>(g, w.b, w.h, row, G, d, acc, M, L);
+                    } else {
+                        if (d == 0) g.part_ml[slot + row] = make_float2(M, L);
+                        *reinterpret_cast<float4*>(g.part_o + (slot + row) * D + d) = acc;
+                    }
                 }
+                if (n + 1 < NB) consumers_sync<32 * kConsumers>();
             }
             ++piece;
         }
@@ -792,13 +843,14 @@ sq_status make_map_pages(CUtensorMap* map, const void* base, int64_t slabs, int 
     return SQ_OK;
 }
 
-int row_tiles(int64_t rows) { return rows <= 16 ? 1 : rows <= 32 ? 2 : rows <= 64 ? 4 : 8; }
+// Rows that the kernel's row tiles hold: 8, or 16 times a power of two.
+int padded_rows(int64_t rows) { return rows <= 8 ? 8 : rows <= 16 ? 16 : rows <= 32 ? 32 : rows <= 64 ? 64 : 128; }
 
 struct KvAttnLayout {
     size_t start, ml, o, total;
 };
 KvAttnLayout kv_attn_layout(int ctas, int64_t rows, int D) {
-    const size_t slots = (size_t)ctas * 2 * 16 * row_tiles(rows);
+    const size_t slots = (size_t)ctas * 2 * padded_rows(rows);
     KvAttnLayout L{};
     L.start = align256((size_t)(ctas + 1) * sizeof(int64_t));
     L.ml = L.start + align256((size_t)ctas * sizeof(int4));
@@ -807,28 +859,29 @@ KvAttnLayout kv_attn_layout(int ctas, int64_t rows, int D) {
     return L;
 }
 
-template <typename T, int D, int MT>
+template <typename T, int D, int NB, int MT>
 sq_status launch_kv_attention(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& g, cudaStream_t st) {
     static bool attr_done[64] = {};
     const DeviceInfo& di = device_info();
-    constexpr size_t smem = AttnSmem<T, D, MT>::TOTAL;
-    sq_status r = ensure_smem_attr(kv_attention_kernel<T, D, MT>, smem, attr_done[di.device & 63]);
+    constexpr size_t smem = AttnSmem<T, D, NB, MT>::TOTAL;
+    sq_status r = ensure_smem_attr(kv_attention_kernel<T, D, NB, MT>, smem, attr_done[di.device & 63]);
     if (r != SQ_OK) return r;
-    r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, MT>, dim3(di.sm_count), dim3(kAttnThreads), smem, st, 1,
+    r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, NB, MT>, dim3(di.sm_count), dim3(attn_threads(NB)), smem, st, 1,
                    mk, mv, g);
     if (r != SQ_OK) return r;
     const int rows = g.n_q_heads / g.c.n_heads * g.q_len;
     return launch_pdl("kv_attention_join_kernel", kv_attention_join_kernel<T, D>, dim3(di.sm_count - 1, (rows + 3) / 4),
-                      dim3(128), 0, st, 1, g, di.sm_count, 16 * MT);
+                      dim3(128), 0, st, 1, g, di.sm_count, 8 * NB * MT);
 }
 
 template <typename T, int D>
 sq_status launch_kv_attention_rows(const CUtensorMap& mk, const CUtensorMap& mv, const KvAttnArgs& g, cudaStream_t st) {
-    switch (row_tiles((int64_t)g.n_q_heads / g.c.n_heads * g.q_len)) {
-    case 1: return launch_kv_attention<T, D, 1>(mk, mv, g, st);
-    case 2: return launch_kv_attention<T, D, 2>(mk, mv, g, st);
-    case 4: return launch_kv_attention<T, D, 4>(mk, mv, g, st);
-    default: return launch_kv_attention<T, D, 8>(mk, mv, g, st);
+    switch (padded_rows((int64_t)g.n_q_heads / g.c.n_heads * g.q_len)) {
+    case 8: return launch_kv_attention<T, D, 1, 1>(mk, mv, g, st);
+    case 16: return launch_kv_attention<T, D, 2, 1>(mk, mv, g, st);
+    case 32: return launch_kv_attention<T, D, 2, 2>(mk, mv, g, st);
+    case 64: return launch_kv_attention<T, D, 2, 4>(mk, mv, g, st);
+    default: return launch_kv_attention<T, D, 2, 8>(mk, mv, g, st);
     }
 }
 
