@@ -1,6 +1,7 @@
 // sq_prompt_attention.cu -- attention of packed prompts over themselves
 // (sq_prompt_attention). Included into the library's single translation unit
 // after sq_kv_attention.cu, some of whose helpers it uses.
+#include <cuda.h>
 #include <cuda_runtime.h>
 
 #include "sq_device.cuh"
@@ -10,50 +11,439 @@ namespace sq {
 namespace {
 
 struct PromptArgs {
-    const __nv_bfloat16 *q, *k, *v;
     __nv_bfloat16* out;
     float* lse;
     const int32_t* cu;
-    int64_t q_stride, k_stride, v_stride, T;
-    int n_seqs, n_q_heads, n_kv_heads;
-    float scale;
+    int64_t T;
+    int n_seqs, n_q_heads, group;   // query heads of one key head
+    float scale;                    // in units of log2
     bool causal;
+    long long wait_limit;
 };
 
-// One warp for each (token, query head).
+// The kernel. A work item is 256 query rows (two tiles of 128) of one sequence and head; the
+// CTAs, one on each SM, take the items in turn, each sequence's longest first. With S = Q K^T and
+// O += P V as tcgen05 products of 128 x 128 x D and 128 x D x 128 and about as much time
+// for the 128 x 128 exponentials of a tile as for its two products, the two query
+// tiles alternate: while one's softmax runs, the other's products do.
+//   Tensor memory: the two tiles' scores (128 columns each, the weights in bf16 over them:
+// P is read as an operand from there) and accumulators (D columns each).
+//   Softmax: a thread has a row. The reference m is moved only when a score is 2^8
+// above it (any row of the warp), so the accumulator is rarely rescaled: P is at most 2^8,
+// and sums and accumulators in fp32 do not care. P is rounded to bf16 (relative
+// 2^-8 at most) because the product takes two bf16 operands.
+//   Warps 0-3 and 4-7: softmax and results of the two tiles. Warp 8 loads (TMA: Q, and K
+// and V tiles of 128 tokens in a ring), warp 9 issues the products.
+constexpr int kPThreads = 384;
+constexpr int kPSlots = 4;              // ring slots, each a K or a V tile
+// registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
+constexpr int kPSoftRegs = 224, kPOtherRegs = 56;
+constexpr float kPSlack = 8.0f;
+
 template <int D>
-__global__ void __launch_bounds__(128) prompt_attention_kernel(const PromptArgs g) {
-    constexpr int E = D / 32;
+struct PromptSmem {
+    static constexpr int BOX = 128 * 128;              // 128 rows of 64 channels
+    static constexpr int TILE = BOX * (D / 64);
+    static constexpr int RING = 2 * TILE;              // behind the two query tiles
+    static constexpr int TOTAL = 1024 + 2 * TILE + kPSlots * TILE;
+};
+
+// O += P V with P in tensor memory.
+__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t"
+                 "setp.ne.b32 p, %4, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
+                 : "memory");
+}
+// A tile whose rows are the contraction: 128-byte swizzled rows of 64 columns, groups of 8
+// rows 1024 bytes apart (stride offset), the next 64 columns a box further (leading offset).
+__device__ __forceinline__ uint64_t make_sw128_rows_desc(uint32_t smem_addr, uint32_t box_bytes) {
+    return make_sw128_kmajor_desc(smem_addr) - ((uint64_t)1 << 16) + ((uint64_t)(box_bytes >> 4) << 16);
+}
+__device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0],"
+        " {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+        "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};"
+        :: "r"(taddr), "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+           "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]),
+           "r"(r[16]), "r"(r[17]), "r"(r[18]), "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]),
+           "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]), "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+__device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+
+// Work items in order: every role walks them alike.
+struct PromptWalk {
+    int64_t f0 = 0;        // blocks of the sequences before b
+    int b = -1, start = 0, len = 0, nb = 0;
+    int h, row;            // head; first query row, in the sequence
+    int n[2];              // key tiles of the two query tiles
+    __device__ __forceinline__ bool find(const PromptArgs& g, int64_t id) {
+        const int64_t f = id / g.n_q_heads;
+        h = (int)(id % g.n_q_heads);
+        while (f >= f0 + nb) {
+            f0 += nb;
+            if (++b >= g.n_seqs) return false;
+            const int64_t a = __ldg(g.cu + b), e = __ldg(g.cu + b + 1);
+            start = (int)min(max(a, (int64_t)0), g.T);
+            len = (int)(min(max(e, (int64_t)start), g.T) - start);
+            nb = (len + 255) / 256;
+        }
+        row = (nb - 1 - (int)(f - f0)) * 256;
+#pragma unroll
+        for (int i = 0; i < 2; ++i) {
+            const int r = row + 128 * i;
+            n[i] = r >= len ? 0 : (min(len, g.causal ? r + 128 : len) + 127) / 128;
+        }
+        return true;
+    }
+};
+
+template <int D>
+__global__ void __launch_bounds__(kPThreads, 1)
+prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_constant__ CUtensorMap map_k,
+                        const __grid_constant__ CUtensorMap map_v, const PromptArgs g) {
+    using S = PromptSmem<D>;
+    constexpr int NBOX = D / 64;
+    extern __shared__ uint8_t smem_raw[];
+    __shared__ __align__(8) uint64_t bars[2 + 2 * kPSlots + 6 + 1];
+    __shared__ uint32_t tmem_base_s;
+    __shared__ int abort_flag, drain_flag;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
+    uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
+    const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, full = q_full + 16, empty = full + 8 * kPSlots;
+    const uint32_t s_full = empty + 8 * kPSlots, p_full = s_full + 16, o_full = p_full + 16, drained = o_full + 16;
+    if (tid == 0) {
+        mbar_init(q_full, 1);
+        mbar_init(q_empty, 1);
+        for (int i = 0; i < kPSlots; ++i) {
+            mbar_init(full + 8 * i, 1);
+            mbar_init(empty + 8 * i, 1);
+        }
+        for (int i = 0; i < 2; ++i) {
+            mbar_init(s_full + 8 * i, 1);
+            mbar_init(p_full + 8 * i, 4);
+            mbar_init(o_full + 8 * i, 1);
+        }
+        mbar_init(drained, 1);
+        abort_flag = 0;
+        drain_flag = 0;
+        fence_barrier_init();
+        tma_prefetch_desc(&map_q);
+        tma_prefetch_desc(&map_k);
+        tma_prefetch_desc(&map_v);
+    }
+    if (warp == 9) tmem_alloc<512>(smem_u32(&tmem_base_s));
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    const uint32_t tmem = tmem_base_s;
+    const uint32_t t_s = tmem, t_o = tmem + 256;   // scores at 0, 128; accumulators at 256, 256 + D
+    const long long limit = g.wait_limit;
+    volatile int* abort = &abort_flag;
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int64_t id = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int h = (int)(id % g.n_q_heads);
-    const int64_t t = id / g.n_q_heads;
-    if (t >= min(g.T, (int64_t)__ldg(g.cu + g.n_seqs))) return;
-    const int b = warp_find([&](int i) { return (int64_t)__ldg(g.cu + i); }, g.n_seqs, t);
-    if (lane == 0 && (__ldg(g.cu + b) < 0 || __ldg(g.cu + b + 1) > g.T)) record_status(SQ_ERR_BOUNDS, SITE_PROMPT);
-    const int64_t u0 = max(0, __ldg(g.cu + b));
-    const int64_t u1 = g.causal ? t + 1 : min(g.T, (int64_t)__ldg(g.cu + b + 1));
-    const int hk = h / (g.n_q_heads / g.n_kv_heads);
-    float x[E], o[E];
-    for (int e = 0; e < E; ++e) {
-        x[e] = to_f32(g.q[t * g.q_stride + (int64_t)h * D + lane * E + e]) * g.scale;
-        o[e] = 0.0f;
+    PromptWalk w;
+
+    if (warp >= 8) {
+        asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPOtherRegs));
+        if (warp == 8) {
+            // ------------------------------------------------------------ loads
+            if (lane == 0) {
+                int slot = 0, work = 0;
+                uint32_t turn = 0;
+                int64_t issued = 0;
+                bool ok = true;
+                if (blockIdx.x == 0)   // once: offsets that the walk cuts
+                    for (int b = 0; b <= g.n_seqs; ++b) {
+                        const int64_t a = __ldg(g.cu + b);
+                        if (a < 0 || a > g.T || (b > 0 && a < __ldg(g.cu + b - 1))) { record_status(SQ_ERR_BOUNDS, SITE_PROMPT); break; }
+                    }
+                auto send = [&](const CUtensorMap* map, int h, int tok) {
+                    if (turn > 0 && !mbar_wait(empty + 8 * slot, (turn - 1) & 1, limit, abort, SITE_PROMPT_WAIT)) return false;
+                    mbar_arrive_expect_tx(full + 8 * slot, S::TILE);
+#pragma unroll
+                    for (int c = 0; c < NBOX; ++c)
+                        tma_load_3d(base + S::RING + slot * S::TILE + c * S::BOX, map, full + 8 * slot, 64 * c, h, tok);
+                    ++issued;
+                    if (++slot == kPSlots) {
+                        slot = 0;
+                        ++turn;
+                    }
+                    return true;
+                };
+                for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x, ++work) {
+                    if (work > 0 && !mbar_wait(q_empty, (work - 1) & 1, limit, abort, SITE_PROMPT_WAIT)) break;
+                    const int tiles = w.n[1] > 0 ? 2 : 1;
+                    mbar_arrive_expect_tx(q_full, tiles * S::TILE);
+                    for (int i = 0; i < tiles; ++i)
+#pragma unroll
+                        for (int c = 0; c < NBOX; ++c)
+                            tma_load_3d(base + i * S::TILE + c * S::BOX, &map_q, q_full, 64 * c, w.h, w.start + w.row + 128 * i);
+                    const int n = max(w.n[0], w.n[1]), hk = w.h / g.group;
+                    for (int j = 0; ok && j < n; ++j) ok = send(&map_k, hk, w.start + 128 * j) && send(&map_v, hk, w.start + 128 * j);
+                }
+                if (*abort) {   // a wait ran out: the copies in flight end before the shared memory goes
+                    volatile int* drain = &drain_flag;
+                    for (int64_t i = issued > kPSlots ? issued - kPSlots : 0; i < issued; ++i)
+                        mbar_wait(full + 8 * (int)(i % kPSlots), (i / kPSlots) & 1, limit, drain, SITE_PROMPT_WAIT);
+                    if (work > 0 || issued > 0) mbar_wait(q_full, (work - 1) & 1, limit, drain, SITE_PROMPT_WAIT);
+                }
+            }
+            __syncwarp();
+        } else if (warp == 9) {
+            // ------------------------------------------------------------ products
+            constexpr uint32_t IS = make_idesc_bf16(128, 128);
+            constexpr uint32_t IO = make_idesc_bf16(128, D) | (1u << 16);   // V's rows are the contraction
+            int slot = 0, work = 0;
+            uint32_t turn = 0;
+            uint32_t p_turn[2] = {0, 0};
+            bool ok = true;
+            int k_slot = 0, v_slot = 0;
+            auto take = [&](int& at) {   // the next ring slot, once it is there
+                at = slot;
+                const bool there = mbar_wait(full + 8 * slot, turn & 1, limit, abort, SITE_PROMPT_WAIT);
+                if (++slot == kPSlots) {
+                    slot = 0;
+                    ++turn;
+                }
+                return (bool)__all_sync(0xffffffffu, there);
+            };
+            auto scores = [&](int i) {   // S_i = Q_i K^T from k_slot
+                if (lane != 0) return;
+#pragma unroll
+                for (int k = 0; k < D / 16; ++k)
+                    mma_bf16(t_s + 128 * i, make_sw128_kmajor_desc(base + i * S::TILE + (k >> 2) * S::BOX + (k & 3) * 32),
+                             make_sw128_kmajor_desc(base + S::RING + k_slot * S::TILE + (k >> 2) * S::BOX + (k & 3) * 32), IS, k > 0);
+                mma_commit(s_full + 8 * i);
+            };
+            for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x, ++work) {
+                const int n = max(w.n[0], w.n[1]);
+                ok = __all_sync(0xffffffffu, mbar_wait(q_full, work & 1, limit, abort, SITE_PROMPT_WAIT)) && take(k_slot);
+                if (!ok) break;
+                tc_fence_after();
+                scores(0);
+                if (w.n[1] > 0) scores(1);
+                if (lane == 0) {
+                    mma_commit(empty + 8 * k_slot);
+                    if (n == 1) mma_commit(q_empty);
+                }
+                for (int j = 0; ok && j < n; ++j) {
+                    ok = take(v_slot);
+                    if (!ok) break;
+                    const int rows = w.len - 128 * j;
+                    if (rows < 128) {   // rows behind the sequence: a weight of 0 times what lies there must be 0
+                        uint8_t* v = base_ptr + S::RING + v_slot * S::TILE;
+                        for (int u = rows * 8 + lane; u < 128 * 8; u += 32)
+#pragma unroll
+                            for (int c = 0; c < NBOX; ++c) *reinterpret_cast<uint4*>(v + c * S::BOX + u * 16) = make_uint4(0, 0, 0, 0);
+                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                        __syncwarp();
+                    }
+                    if (j + 1 < n) ok = take(k_slot);
+                    for (int i = 0; ok && i < 2; ++i) {
+                        if (j < w.n[i]) {
+                            // the weights are there; on a new item this also says that the same
+                            // warps have read the last one's accumulator
+                            ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * i, p_turn[i] & 1, limit, abort, SITE_PROMPT_WAIT));
+                            if (!ok) break;
+                            ++p_turn[i];
+                            tc_fence_after();
+                            if (lane == 0) {
+#pragma unroll
+                                for (int k = 0; k < 8; ++k)
+                                    mma_bf16_ta(t_o + D * i, t_s + 128 * i + 8 * k,
+                                                make_sw128_rows_desc(base + S::RING + v_slot * S::TILE + k * 2048, S::BOX), IO, j > 0 || k > 0);
+                                if (j + 1 == w.n[i]) mma_commit(o_full + 8 * i);
+                            }
+                        }
+                        if (i == 1 && lane == 0) mma_commit(empty + 8 * v_slot);
+                        if (j + 1 < w.n[i]) scores(i);
+                    }
+                    if (ok && j + 1 < n && lane == 0) {
+                        mma_commit(empty + 8 * k_slot);
+                        if (j + 2 == n) mma_commit(q_empty);
+                    }
+                }
+            }
+            if (*abort) {   // products in flight end before the tensor memory goes
+                if (lane == 0) {
+                    volatile int* drain = &drain_flag;
+                    mma_commit(drained);
+                    mbar_wait(drained, 0, limit, drain, SITE_PROMPT_WAIT);
+                }
+            }
+            __syncwarp();
+        }
+    } else {
+        // ---------------------------------------------------------------- softmax
+        asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPSoftRegs));
+        const int i = warp >> 2;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
+        const uint32_t ts = t_s + 128 * i + lanes, to = t_o + D * i + lanes;
+        const float sc = g.scale;
+        const bool neg = sc < 0.0f;
+        uint32_t s_turn = 0, o_turn = 0;
+        bool ok = true;
+        for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x) {
+            const int n = w.n[i];
+            if (n == 0) continue;
+            const int r = w.row + 128 * i + (tid & 127);      // this thread's row, in the sequence
+            const int see = g.causal ? min(r + 1, w.len) : w.len;
+            const int sure = g.causal ? min(w.row + 128 * i + 1, w.len) : w.len;   // what every row of the tile sees
+            float m = kNoReference, l = 0.0f;
+            for (int j = 0; j < n; ++j) {
+                ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * i, s_turn & 1, limit, abort, SITE_PROMPT_WAIT));
+                if (!ok) break;
+                ++s_turn;
+                tc_fence_after();
+                uint32_t x[4][32];
+#pragma unroll
+                for (int c = 0; c < 4; ++c) tmem_ld_32x32b_x32(ts + 32 * c, x[c]);
+                tmem_wait_ld();
+                if (128 * j + 128 > sure) {
+                    const int v = see - 128 * j;   // columns this row sees
+                    const uint32_t none = neg ? 0x7f800000u : 0xff800000u;
+#pragma unroll
+                    for (int c = 0; c < 4; ++c)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (32 * c + e >= v) x[c][e] = none;
+                }
+                float t[4];
+                if (neg) {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        t[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                        for (int e = 1; e < 32; ++e) t[c] = fminf(t[c], __uint_as_float(x[c][e]));
+                    }
+                    t[0] = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
+                } else {
+#pragma unroll
+                    for (int c = 0; c < 4; ++c) {
+                        t[c] = __uint_as_float(x[c][0]);
+#pragma unroll
+                        for (int e = 1; e < 32; ++e) t[c] = fmaxf(t[c], __uint_as_float(x[c][e]));
+                    }
+                    t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
+                }
+                const float top = t[0] * sc;
+                if (__any_sync(0xffffffffu, top > m + kPSlack)) {
+                    const float mn = fmaxf(m, top);
+                    const float f = exp2_fast(m - mn);
+                    m = mn;
+                    if (j > 0) {   // the accumulator: the products before these scores are complete
+                        l *= f;
+#pragma unroll
+                        for (int c = 0; c < D / 32; ++c) {
+                            uint32_t o[32];
+                            tmem_ld_32x32b_x32(to + 32 * c, o);
+                            tmem_wait_ld();
+#pragma unroll
+                            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st_32x32b_x32(to + 32 * c, o);
+                        }
+                    }
+                }
+                const uint64_t sc2 = f2_pack(sc, sc), m2 = f2_pack(-m, -m);
+                uint64_t sum[4] = {0, 0, 0, 0};
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    uint32_t pk[32];
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) {
+                        const int c = 2 * half + (e >> 4), k = (2 * e) & 31;
+                        float a, b;
+                        f2_unpack(pair_fma(f2_pack(__uint_as_float(x[c][k]), __uint_as_float(x[c][k + 1])), sc2, m2), a, b);
+                        a = exp2_fast(a);
+                        b = exp2_fast(b);
+                        sum[e & 3] = f2_add(sum[e & 3], f2_pack(a, b));
+                        pk[e] = pack_bf16x2(a, b);
+                    }
+                    tmem_st_32x32b_x32(ts + 32 * half, pk);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(p_full + 8 * i);
+                float a, b;
+                f2_unpack(f2_add(f2_add(sum[0], sum[1]), f2_add(sum[2], sum[3])), a, b);
+                l += a + b;
+            }
+            if (!ok) break;
+            ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * i, o_turn & 1, limit, abort, SITE_PROMPT_WAIT));
+            if (!ok) break;
+            ++o_turn;
+            tc_fence_after();
+            const float inv = 1.0f / l;
+            const int64_t at = (int64_t)(w.start + r) * g.n_q_heads + w.h;
+#pragma unroll
+            for (int c = 0; c < D / 32; ++c) {
+                uint32_t o[32];
+                tmem_ld_32x32b_x32(to + 32 * c, o);
+                tmem_wait_ld();
+                if (r < w.len) {
+                    uint4* dst = reinterpret_cast<uint4*>(g.out + at * D + 32 * c);
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        uint32_t y[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            y[k] = pack_bf16x2(__uint_as_float(o[8 * e + 2 * k]) * inv, __uint_as_float(o[8 * e + 2 * k + 1]) * inv);
+                        dst[e] = make_uint4(y[0], y[1], y[2], y[3]);
+                    }
+                }
+            }
+            if (g.lse && r < w.len) g.lse[at] = 0.6931471805599453f * (m + log2f(l));
+            tc_fence_before();
+        }
     }
-    float m = -INFINITY, l = 0.0f;
-    for (int64_t u = u0; u < u1; ++u) {
-        float s = 0.0f;
-        for (int e = 0; e < E; ++e) s += x[e] * to_f32(g.k[u * g.k_stride + (int64_t)hk * D + lane * E + e]);
-        for (int d = 16; d > 0; d >>= 1) s += __shfl_xor_sync(0xffffffffu, s, d);
-        const float mn = fmaxf(m, s);
-        const float f = expf(m - mn), w = expf(s - mn);
-        m = mn;
-        l = l * f + w;
-        for (int e = 0; e < E; ++e) o[e] = o[e] * f + w * to_f32(g.v[u * g.v_stride + (int64_t)hk * D + lane * E + e]);
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 9) {
+        tc_fence_after();
+        tmem_dealloc<512>(tmem);
     }
-    for (int e = 0; e < E; ++e) put(g.out + (t * g.n_q_heads + h) * D + lane * E + e, l > 0.0f ? o[e] / l : 0.0f);
-    if (g.lse && lane == 0) g.lse[t * g.n_q_heads + h] = l > 0.0f ? m + logf(l) : -INFINITY;
+}
+
+// Tokens [T][heads][D] bf16, `stride` elements from token to token, as a map whose box is 64
+// channels of one head of 128 tokens.
+sq_status make_map_tokens(CUtensorMap* map, const void* base, int64_t T, int64_t heads, int64_t D, int64_t stride) {
+    sq_status r = get_encoder();
+    if (r != SQ_OK) return r;
+    cuuint64_t dims[3] = {(cuuint64_t)D, (cuuint64_t)heads, (cuuint64_t)T};
+    cuuint64_t strides[2] = {(cuuint64_t)D * 2, (cuuint64_t)stride * 2};
+    cuuint32_t box[3] = {64u, 1u, 128u};
+    cuuint32_t estr[3] = {1, 1, 1};
+    CUresult cr = g_encode(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(base), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    if (cr != CUDA_SUCCESS) {
+        set_error("cuTensorMapEncodeTiled failed (%d) for %lld tokens of %lld heads", (int)cr, (long long)T, (long long)heads);
+        return SQ_ERR_CUDA;
+    }
+    return SQ_OK;
+}
+
+template <int D>
+sq_status launch_prompt(const CUtensorMap& mq, const CUtensorMap& mk, const CUtensorMap& mv, const PromptArgs& g, cudaStream_t st) {
+    static bool attr_done[64] = {};
+    const DeviceInfo& di = device_info();
+    constexpr size_t smem = PromptSmem<D>::TOTAL;
+    sq_status r = ensure_smem_attr(prompt_attention_kernel<D>, smem, attr_done[di.device & 63]);
+    if (r != SQ_OK) return r;
+    const int64_t items = (g.T / 256 + g.n_seqs) * g.n_q_heads;   // at most
+    const unsigned grid = (unsigned)(items < di.sm_count ? items : di.sm_count);
+    return launch_pdl("prompt_attention_kernel", prompt_attention_kernel<D>, dim3(grid), dim3(kPThreads), smem, st, 1, mq, mk, mv, g);
 }
 
 sq_status prompt_attention_impl(const void* q, int64_t q_stride, const void* k, int64_t k_stride, const void* v,
@@ -63,7 +453,7 @@ sq_status prompt_attention_impl(const void* q, int64_t q_stride, const void* k, 
     sq_status r;
     if (n_seqs < 0 || T < 0 || n_q_heads < 0 || n_kv_heads < 0) { set_error("negative size"); return SQ_ERR_INVALID_ARG; }
     if (D != 64 && D != 128) { set_error("head_dim must be 64 or 128 (got %lld)", (long long)D); return SQ_ERR_UNSUPPORTED; }
-    if (!(scale > -3.0e38f && scale < 3.0e38f)) { set_error("scale must be finite"); return SQ_ERR_INVALID_ARG; }
+    if (!(scale >= -1.0e38f && scale <= 1.0e38f)) { set_error("scale must be within +-1e38"); return SQ_ERR_INVALID_ARG; }
     if (n_seqs > 65536 || n_q_heads > 1024 || T > (int64_t(1) << 30) / (n_q_heads > 0 ? n_q_heads : 1)) {
         set_error("n_seqs, n_q_heads or T too large");
         return SQ_ERR_UNSUPPORTED;
@@ -78,12 +468,16 @@ sq_status prompt_attention_impl(const void* q, int64_t q_stride, const void* k, 
     if ((r = check_rows(v, v_stride, n_kv_heads * D, 2, "v")) != SQ_OK) return r;
     if (!cu || !out) { set_error("cu_seqlens or out: NULL pointer"); return SQ_ERR_INVALID_ARG; }
     if (!aligned16(out)) { set_error("out must be 16-byte aligned"); return SQ_ERR_UNSUPPORTED; }
-    PromptArgs g{static_cast<const __nv_bfloat16*>(q), static_cast<const __nv_bfloat16*>(k),
-                 static_cast<const __nv_bfloat16*>(v), static_cast<__nv_bfloat16*>(out), lse, cu, q_stride, k_stride,
-                 v_stride, T, (int)n_seqs, (int)n_q_heads, (int)n_kv_heads, scale, causal != 0};
-    const dim3 grid((unsigned)((T * n_q_heads + 3) / 4)), block(128);
-    return D == 64 ? launch_pdl("prompt_attention_kernel", prompt_attention_kernel<64>, grid, block, 0, st, 1, g)
-                   : launch_pdl("prompt_attention_kernel", prompt_attention_kernel<128>, grid, block, 0, st, 1, g);
+    // A scale of 0 weighs all tokens alike; a smaller factor than any score times it can
+    // show keeps masked scores at -infinity.
+    const float sc = (scale == 0.0f ? 1.0e-37f : scale) * 1.4426950408889634f;
+    PromptArgs g{static_cast<__nv_bfloat16*>(out), lse, cu, T, (int)n_seqs, (int)n_q_heads, (int)(n_q_heads / n_kv_heads), sc,
+                 causal != 0, wait_limit_cycles()};
+    CUtensorMap mq, mk, mv;
+    if ((r = make_map_tokens(&mq, q, T, n_q_heads, D, q_stride)) != SQ_OK) return r;
+    if ((r = make_map_tokens(&mk, k, T, n_kv_heads, D, k_stride)) != SQ_OK) return r;
+    if ((r = make_map_tokens(&mv, v, T, n_kv_heads, D, v_stride)) != SQ_OK) return r;
+    return D == 64 ? launch_prompt<64>(mq, mk, mv, g, st) : launch_prompt<128>(mq, mk, mv, g, st);
 }
 
 }  // namespace
