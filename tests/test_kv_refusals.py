@@ -21,7 +21,7 @@ ST = ctypes.c_void_p(0)
 def cache(sq, **over):
     f = dict(k=0x1000, v=0x1000, k_scale=0x1000, v_scale=0x1000, n_pages=10, n_heads=4, head_dim=128, page_size=64, scale_block=16)
     f.update(over)
-    return ctypes.byref(sq._KvCacheStruct(*f.values()))
+    return sq._KV_CACHE.pack(*f.values())
 
 
 BAD_CACHES = [
@@ -103,7 +103,7 @@ def test_bad_table(sq):
     inv, uns = sq.SQ_ERR_INVALID_ARG, sq.SQ_ERR_UNSUPPORTED
 
     def table(out=P, first=0, n=4, rot=128, theta=1e4, sc=None):
-        s = None if sc is None else ctypes.byref(sq._RopeScaling(*sc))
+        s = None if sc is None else sq._ROPE_SCALING.pack(*sc)
         return sq.raw_status("sq_rope_table", out, first, n, rot, ctypes.c_double(theta), s, ST)
 
     for kw, want in [(dict(first=-1), inv), (dict(n=-1), inv), (dict(rot=24), uns), (dict(rot=0), uns), (dict(rot=272), uns),
@@ -125,4 +125,4 @@ def test_the_binding_checks_shapes_before_the_call(sq):
         sq.sq_kv_attention(torch.zeros((1, 1, 1, 64)), c, torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
     c = sq.KvCache.empty(2, 1, 64, 16, 16, device="cpu")
     with pytest.raises(ValueError, match="same shapes"):
-        sq._cache_struct(sq.KvCache(c.k, c.v[:1], c.k_scale, c.v_scale))
+        sq._cache_bytes(sq.KvCache(c.k, c.v[:1], c.k_scale, c.v_scale))

@@ -11,6 +11,7 @@ from __future__ import annotations
 import ctypes
 import os
 import re
+import struct
 import typing
 
 import torch
@@ -536,15 +537,9 @@ def sq_linear(x: torch.Tensor, w: torch.Tensor, alpha: float, eps: float = 1e-8,
     return y
 
 
-class _RopeScaling(ctypes.Structure):
-    _fields_ = [("factor", ctypes.c_double), ("low_turns", ctypes.c_double), ("high_turns", ctypes.c_double),
-                ("original_len", _i64), ("magnitude", ctypes.c_double)]
-
-
-class _KvCacheStruct(ctypes.Structure):
-    _fields_ = [("k", _vp), ("v", _vp), ("k_scale", _vp), ("v_scale", _vp), ("n_pages", _i64),
-                ("n_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("page_size", ctypes.c_int32),
-                ("scale_block", ctypes.c_int32)]
+# C structs as their bytes (host memory that lives for the call)
+_ROPE_SCALING = struct.Struct("dddqd")    # sq_rope_scaling
+_KV_CACHE = struct.Struct("PPPPqiiii")    # sq_kv_cache
 
 
 class KvCache(typing.NamedTuple):
@@ -565,45 +560,53 @@ class KvCache(typing.NamedTuple):
         return cls(*codes, *scales)
 
 
-def _cache_struct(cache: KvCache) -> _KvCacheStruct:
+def _ptr(t: torch.Tensor, dtype, index: int, name: str) -> int:
+    """The address of a contiguous tensor of `dtype` on CUDA device `index`."""
+    if t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
+        if not t.is_cuda:
+            raise ValueError(f"{name} must be a CUDA tensor")
+        if t.dtype is not dtype:
+            raise TypeError(f"{name} must be {dtype}")
+        if not t.is_contiguous():
+            raise ValueError(f"{name} must be contiguous")
+        raise ValueError(f"{name} is on {t.device}, other tensors on cuda:{index}")
+    return t.data_ptr()
+
+
+def _shaped(t: torch.Tensor, shape: tuple, dtype, index: int, name: str) -> int:
+    if t.shape != shape:
+        raise ValueError(f"{name} must have shape {tuple(shape)}, has {tuple(t.shape)}")
+    return _ptr(t, dtype, index, name)
+
+
+def _cache_bytes(cache: KvCache) -> tuple[bytes, int, int, int]:
+    """-> (sq_kv_cache, CUDA device index, n_heads, head_dim)."""
     k, v, ks, vs = cache
-    n_pages, n_heads, page_size, head_dim = k.shape
-    if v.shape != k.shape or vs.shape != ks.shape or ks.dim() != 3 or ks.shape[:2] != k.shape[:2]:
+    n_pages, n_heads, page_size, head_dim = shape = k.shape
+    if v.shape != shape or vs.shape != ks.shape or ks.dim() != 3 or ks.shape[:2] != shape[:2]:
         raise ValueError("cache: k and v, and k_scale and v_scale, must have the same shapes")
     blocks = ks.shape[2]
     if blocks == 0 or page_size % blocks:
         raise ValueError("cache: page_size must be a multiple of the scales per page")
-    if k.dtype != torch.int8 or v.dtype != torch.int8 or ks.dtype != torch.float32 or vs.dtype != torch.float32:
-        raise TypeError("cache: codes are int8, scales float32")
-    return _KvCacheStruct(_dev(k, "cache.k"), _dev(v, "cache.v"), _dev(ks, "cache.k_scale"), _dev(vs, "cache.v_scale"),
-                          n_pages, n_heads, head_dim, page_size, page_size // blocks)
+    index = k.get_device()
+    if index < 0:
+        raise ValueError("cache.k must be a CUDA tensor")
+    return (_KV_CACHE.pack(_ptr(k, torch.int8, index, "cache.k"), _ptr(v, torch.int8, index, "cache.v"),
+                           _ptr(ks, torch.float32, index, "cache.k_scale"), _ptr(vs, torch.float32, index, "cache.v_scale"),
+                           n_pages, n_heads, head_dim, page_size, page_size // blocks), index, n_heads, head_dim)
 
 
-def _same_device(first: torch.Tensor, *others) -> None:
-    for t in others:
-        if t is not None and t.device != first.device:
-            raise ValueError(f"tensors on {first.device} and {t.device}")
-
-
-def _i32(t: torch.Tensor, shape: tuple, name: str) -> int:
-    if t.dtype != torch.int32:
-        raise TypeError(f"{name} must be int32")
-    if tuple(t.shape) != shape:
-        raise ValueError(f"{name} must have shape {shape}, has {tuple(t.shape)}")
-    return _dev(t, name)
-
-
-def _token_rows(t: torch.Tensor, name: str) -> tuple[int, int]:
+def _token_rows(t: torch.Tensor, index: int, name: str) -> tuple[int, int]:
     """(address, elements between tokens) of [.., tokens, heads, head_dim] whose
     heads are contiguous and whose tokens are evenly spaced."""
-    if not t.is_cuda:
-        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.get_device() != index or index < 0:
+        raise ValueError(f"{name} must be a CUDA tensor on the other tensors' device")
     shape, stride = t.shape, t.stride()
-    if t.numel() and ((shape[-1] > 1 and stride[-1] != 1) or (shape[-2] > 1 and stride[-2] != shape[-1])):
+    d, heads = shape[-1], shape[-2]
+    if t.numel() and ((d > 1 and stride[-1] != 1) or (heads > 1 and stride[-2] != d)):
         raise ValueError(f"{name}: the heads of a token must be contiguous")
-    width = shape[-1] * shape[-2]
-    step = stride[-3] if shape[-3] > 1 else width
-    if t.dim() == 4 and shape[0] > 1:
+    step = stride[-3] if shape[-3] > 1 else d * heads
+    if len(shape) == 4 and shape[0] > 1:
         if shape[1] == 1:
             step = stride[0]
         elif stride[0] != shape[1] * step:
@@ -611,31 +614,38 @@ def _token_rows(t: torch.Tensor, name: str) -> tuple[int, int]:
     return t.data_ptr(), step
 
 
-def _made(shape, dtype, device, stream) -> torch.Tensor:
-    """A tensor that the call on `stream` writes; known to the allocator as in
-    use there when that is not the current stream."""
-    t = torch.empty(shape, dtype=dtype, device=device)
+def _made(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
+    """A tensor on like's device that the call on `stream` writes; known to the
+    allocator as in use there when that is not the current stream."""
+    t = like.new_empty(shape, dtype=dtype)
     if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), device))
+        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device))
     return t
 
 
-class _on:
-    """Makes `device` current for a call if it is not, and gives its stream."""
+def _given_or_made(t, like: torch.Tensor, shape, dtype, index: int, stream, name: str):
+    """-> (t, its address); a new tensor if t is None."""
+    if t is None:
+        t = _made(like, shape, dtype, stream)
+        return t, t.data_ptr()
+    return t, _shaped(t, shape, dtype, index, name)
 
-    def __init__(self, device: torch.device, stream):
-        index = device.index if device.index is not None else torch.cuda.current_device()
-        self.guard = torch.cuda.device(index) if index != torch.cuda.current_device() else None
-        self.stream = stream
 
-    def __enter__(self) -> int:
-        if self.guard is not None:
-            self.guard.__enter__()
-        return _stream(self.stream)
-
-    def __exit__(self, *args):
-        if self.guard is not None:
-            self.guard.__exit__(*args)
+def _launch(index: int, stream, name: str, *args) -> None:
+    """Call a C entry point on CUDA device `index`, on `stream` or that device's
+    current stream (the last C argument)."""
+    call = getattr(_lib, name)
+    if stream is None:
+        st = torch._C._cuda_getCurrentRawStream(index)
+    else:
+        st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
+    if torch.cuda.current_device() == index:
+        status = call(*args, st)
+    else:
+        with torch.cuda.device(index):
+            status = call(*args, st)
+    if status != SQ_OK:
+        _check(status, name)
 
 
 def sq_rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, first_pos: int = 0, factor: float = 1.0,
@@ -644,17 +654,19 @@ def sq_rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, first_pos: i
     """cos and sin of the rotary angles, float32 [n_pos, rot_dim / 2, 2];
     frequencies scaled by `factor`, all of them or (high_turns > 0) those that
     make few turns in original_len tokens."""
-    device = table.device if table is not None else torch.device("cuda" if device is None else device)
-    if device.type != "cuda":
-        raise ValueError("the table is a CUDA tensor")
-    if table is not None and (tuple(table.shape) != (n_pos, rot_dim // 2, 2) or table.dtype != torch.float32):
-        raise ValueError(f"table must be float32 [{n_pos}, {rot_dim // 2}, 2]")
-    scaling = _RopeScaling(float(factor), float(low_turns), float(high_turns), int(original_len), float(magnitude))
-    with _on(device, stream) as st:
-        if table is None:
-            table = _made((max(n_pos, 0), max(rot_dim, 0) // 2, 2), torch.float32, device, stream)
-        _check(_lib.sq_rope_table(_dev(table, "table"), first_pos, n_pos, rot_dim, float(theta), ctypes.byref(scaling), st),
-               "sq_rope_table")
+    shape = (max(n_pos, 0), max(rot_dim, 0) // 2, 2)
+    if table is None:
+        device = torch.device("cuda" if device is None else device)
+        if device.type != "cuda":
+            raise ValueError("the table is a CUDA tensor")
+        table = torch.empty(shape, dtype=torch.float32, device=device)
+        if stream is not None:
+            table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
+                                torch.cuda.ExternalStream(int(stream), table.device))
+    index = table.get_device()
+    ptr = _shaped(table, shape, torch.float32, index, "table")
+    scaling = _ROPE_SCALING.pack(factor, low_turns, high_turns, original_len, magnitude)
+    _launch(index, stream, "sq_rope_table", ptr, first_pos, n_pos, rot_dim, theta, scaling)
     return table
 
 
@@ -665,42 +677,36 @@ def sq_rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
     """Rotate q [T, n_q_heads, head_dim] and k, append k and v [T, n_heads,
     head_dim] to the cache -> (rotated q, rotated k or None). The tensors may be
     slices of one QKV output."""
-    c = _cache_struct(cache)
-    T = k.shape[0]
-    if k.shape != v.shape or tuple(k.shape) != (T, c.n_heads, c.head_dim):
-        raise ValueError(f"k and v must be [T, {c.n_heads}, {c.head_dim}]")
-    if v.dtype != k.dtype or (q is not None and q.dtype != k.dtype):
-        raise TypeError("q, k and v must have the same dtype")
-    _same_device(k, q, v, *cache, block_table, ctx_len, cu_new, table, q_out, k_out)
-    n_seqs, max_pages = block_table.shape
+    c, index, heads, d = _cache_bytes(cache)
+    dtype = k.dtype
     dt = _dt(k)
-    with _on(k.device, stream) as st:
-        q_ptr, q_step, hq, qo = None, 0, 0, None
-        if q is not None:
-            if q.dim() != 3 or q.shape[0] != T or q.shape[2] != c.head_dim:
-                raise ValueError(f"q must be [{T}, n_q_heads, {c.head_dim}]")
-            hq = q.shape[1]
-            q_ptr, q_step = _token_rows(q, "q")
-            if q_out is None:
-                q_out = _made((T, hq, c.head_dim), q.dtype, q.device, stream)
-            elif q_out.shape != q.shape or q_out.dtype != q.dtype:
-                raise ValueError("q_out must have q's shape and dtype")
-            qo = _dev(q_out, "q_out")
-        k_ptr, k_step = _token_rows(k, "k")
-        v_ptr, v_step = _token_rows(v, "v")
-        if k_out is None and want_k:
-            k_out = _made((T, c.n_heads, c.head_dim), k.dtype, k.device, stream)
-        elif k_out is not None and (k_out.shape != k.shape or k_out.dtype != k.dtype):
-            raise ValueError("k_out must have k's shape and dtype")
-        t_ptr, n_pos, rot = None, 0, 0
-        if table is not None:
-            if table.dim() != 3 or table.shape[2] != 2 or table.dtype != torch.float32:
-                raise ValueError("table must be float32 [n_pos, rot_dim / 2, 2]")
-            t_ptr, n_pos, rot = _dev(table, "table"), table.shape[0], 2 * table.shape[1]
-        _check(_lib.sq_rope_kv_append(ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"), max_pages,
-                                      _i32(ctx_len, (n_seqs,), "ctx_len"), _i32(cu_new, (n_seqs + 1,), "cu_new"), n_seqs, T,
-                                      q_ptr, q_step, hq, k_ptr, k_step, v_ptr, v_step, dt, t_ptr, n_pos, rot,
-                                      int(interleaved), qo, _opt_dev(k_out, "k_out"), st), "sq_rope_kv_append")
+    T = k.shape[0]
+    if k.shape != (T, heads, d) or v.shape != k.shape:
+        raise ValueError(f"k and v must be [T, {heads}, {d}]")
+    if v.dtype is not dtype or (q is not None and q.dtype is not dtype):
+        raise TypeError("q, k and v must have the same dtype")
+    n_seqs, max_pages = block_table.shape
+    q_ptr, q_step, hq, qo = None, 0, 0, None
+    if q is not None:
+        hq = q.shape[1]
+        if q.shape != (T, hq, d):
+            raise ValueError(f"q must be [{T}, n_q_heads, {d}]")
+        q_ptr, q_step = _token_rows(q, index, "q")
+        q_out, qo = _given_or_made(q_out, q, (T, hq, d), dtype, index, stream, "q_out")
+    k_ptr, k_step = _token_rows(k, index, "k")
+    v_ptr, v_step = _token_rows(v, index, "v")
+    ko = None
+    if k_out is not None or want_k:
+        k_out, ko = _given_or_made(k_out, k, (T, heads, d), dtype, index, stream, "k_out")
+    t_ptr, n_pos, rot = None, 0, 0
+    if table is not None:
+        n_pos, half, _ = table.shape
+        rot = 2 * half
+        t_ptr = _shaped(table, (n_pos, half, 2), torch.float32, index, "table")
+    _launch(index, stream, "sq_rope_kv_append", c, _ptr(block_table, torch.int32, index, "block_table"), max_pages,
+            _shaped(ctx_len, (n_seqs,), torch.int32, index, "ctx_len"),
+            _shaped(cu_new, (n_seqs + 1,), torch.int32, index, "cu_new"), n_seqs, T, q_ptr, q_step, hq, k_ptr, k_step,
+            v_ptr, v_step, dt, t_ptr, n_pos, rot, 1 if interleaved else 0, qo, ko)
     return q_out, k_out
 
 
@@ -708,26 +714,26 @@ def sq_kv_read(cache: KvCache, block_table: torch.Tensor, first: torch.Tensor, c
                dtype=torch.bfloat16, k_out: torch.Tensor | None = None, v_out: torch.Tensor | None = None, stream=None):
     """The cached tokens from first[b] on of every sequence, packed by cu_out
     into n_rows rows -> (k, v) [n_rows, n_heads, head_dim]."""
-    c = _cache_struct(cache)
-    _same_device(cache.k, *cache[1:], block_table, first, cu_out, k_out, v_out)
+    c, index, heads, d = _cache_bytes(cache)
     n_seqs, max_pages = block_table.shape
-    shape = (n_rows, c.n_heads, c.head_dim)
-    with _on(cache.k.device, stream) as st:
-        if k_out is None:
-            k_out = _made(shape, dtype, cache.k.device, stream)
-        if v_out is None:
-            v_out = _made(shape, k_out.dtype, cache.k.device, stream)
-        if tuple(k_out.shape) != shape or tuple(v_out.shape) != shape or k_out.dtype != v_out.dtype:
-            raise ValueError(f"k_out and v_out must be {shape} and of one dtype")
-        _check(_lib.sq_kv_read(ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"), max_pages,
-                               _i32(first, (n_seqs,), "first"), _i32(cu_out, (n_seqs + 1,), "cu_out"), n_seqs, n_rows,
-                               _dev(k_out, "k_out"), _dev(v_out, "v_out"), _dt(k_out), st), "sq_kv_read")
+    shape = (n_rows, heads, d)
+    if k_out is not None:
+        dtype = k_out.dtype
+    elif v_out is not None:
+        dtype = v_out.dtype
+    k_out, ko = _given_or_made(k_out, cache.k, shape, dtype, index, stream, "k_out")
+    v_out, vo = _given_or_made(v_out, cache.k, shape, dtype, index, stream, "v_out")
+    _launch(index, stream, "sq_kv_read", c, _ptr(block_table, torch.int32, index, "block_table"), max_pages,
+            _shaped(first, (n_seqs,), torch.int32, index, "first"),
+            _shaped(cu_out, (n_seqs + 1,), torch.int32, index, "cu_out"), n_seqs, n_rows,
+            ko, vo, _dt(k_out))
     return k_out, v_out
 
 
 def sq_kv_attention_workspace_size(cache: KvCache, n_seqs: int, q_len: int, n_q_heads: int) -> int:
-    with _on(cache.k.device, None):
-        return int(_lib.sq_kv_attention_workspace_size(ctypes.byref(_cache_struct(cache)), n_seqs, q_len, n_q_heads))
+    c, index, _, _ = _cache_bytes(cache)
+    with torch.cuda.device(index):
+        return int(_lib.sq_kv_attention_workspace_size(c, n_seqs, q_len, n_q_heads))
 
 
 def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_len: torch.Tensor,
@@ -736,31 +742,31 @@ def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, 
     """The newest q_len tokens' q [n_seqs, q_len, n_q_heads, head_dim] over the
     cached tokens of their sequences -> out, or (out, lse) if asked for. `scale`
     is head_dim ** -0.5 if not given."""
-    c = _cache_struct(cache)
-    if q.dim() != 4 or q.shape[3] != c.head_dim:
-        raise ValueError(f"q must be [n_seqs, q_len, n_q_heads, {c.head_dim}]")
-    n_seqs, q_len, hq, d = q.shape
-    max_pages = block_table.shape[1]
-    _same_device(q, *cache, block_table, seq_len, out, lse, workspace)
+    c, index, _, d = _cache_bytes(cache)
+    shape = q.shape
+    if len(shape) != 4 or shape[3] != d:
+        raise ValueError(f"q must be [n_seqs, q_len, n_q_heads, {d}]")
+    n_seqs, q_len, hq, _ = shape
+    dtype = q.dtype
     dt = _dt(q)
-    with _on(q.device, stream) as st:
-        q_ptr, q_step = _token_rows(q, "q")
-        if out is None:
-            out = _made((n_seqs, q_len, hq, d), q.dtype, q.device, stream)
-        elif out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must have q's shape and dtype")
-        if lse is None and want_lse:
-            lse = _made((n_seqs, q_len, hq), torch.float32, q.device, stream)
-        elif lse is not None and (tuple(lse.shape) != (n_seqs, q_len, hq) or lse.dtype != torch.float32):
-            raise ValueError("lse must be float32 [n_seqs, q_len, n_q_heads]")
-        if workspace is None:
-            need = int(_lib.sq_kv_attention_workspace_size(ctypes.byref(c), n_seqs, q_len, hq))
-            workspace = _made((need,), torch.uint8, q.device, stream)
-        _check(_lib.sq_kv_attention(q_ptr, q_step, dt, ctypes.byref(c), _i32(block_table, (n_seqs, max_pages), "block_table"),
-                                    max_pages, _i32(seq_len, (n_seqs,), "seq_len"), n_seqs, q_len, hq,
-                                    float(d ** -0.5 if scale is None else scale), _dev(out, "out"), _opt_dev(lse, "lse"),
-                                    _dev(workspace, "workspace"), workspace.numel() * workspace.element_size(), st),
-               "sq_kv_attention")
+    q_ptr, q_step = _token_rows(q, index, "q")
+    max_pages = block_table.shape[1]
+    out, o_ptr = _given_or_made(out, q, shape, dtype, index, stream, "out")
+    l_ptr = None
+    if lse is not None or want_lse:
+        lse, l_ptr = _given_or_made(lse, q, (n_seqs, q_len, hq), torch.float32, index, stream, "lse")
+    if workspace is None:
+        # the size goes by the device's SMs, which are alike on every device of a node
+        ws_bytes = _lib.sq_kv_attention_workspace_size(c, n_seqs, q_len, hq)
+        workspace = _made(q, (ws_bytes,), torch.uint8, stream)
+        ws = workspace.data_ptr()
+    else:
+        ws_bytes = workspace.numel()
+        ws = _ptr(workspace, torch.uint8, index, "workspace")
+    _launch(index, stream, "sq_kv_attention", q_ptr, q_step, dt, c,
+            _shaped(block_table, (n_seqs, max_pages), torch.int32, index, "block_table"), max_pages,
+            _shaped(seq_len, (n_seqs,), torch.int32, index, "seq_len"), n_seqs, q_len, hq,
+            d ** -0.5 if scale is None else scale, o_ptr, l_ptr, ws, ws_bytes)
     return out if lse is None else (out, lse)
 
 
@@ -770,27 +776,24 @@ def sq_prompt_attention(q: torch.Tensor, k: torch.Tensor, v: torch.Tensor, cu_se
     """Packed prompts q [T, n_q_heads, head_dim], k, v [T, n_kv_heads, head_dim]
     (bf16; slices of one QKV output may be given) over themselves -> out, or
     (out, lse) if asked for. `scale` is head_dim ** -0.5 if not given."""
-    if q.dim() != 3 or k.dim() != 3 or k.shape != v.shape or k.shape[0] != q.shape[0] or k.shape[2] != q.shape[2]:
+    shape = q.shape
+    T, hq, d = shape
+    heads = k.shape[1]
+    if k.shape != (T, heads, d) or v.shape != k.shape:
         raise ValueError("q must be [T, n_q_heads, head_dim], k and v [T, n_kv_heads, head_dim]")
-    if any(t.dtype != torch.bfloat16 for t in (q, k, v)):
+    if q.dtype is not torch.bfloat16 or k.dtype is not torch.bfloat16 or v.dtype is not torch.bfloat16:
         raise TypeError("q, k and v must be bfloat16")
-    _same_device(q, k, v, cu_seqlens, out, lse)
-    T, hq, d = q.shape
+    index = q.get_device()
+    (q_ptr, q_step), (k_ptr, k_step), (v_ptr, v_step) = (_token_rows(q, index, "q"), _token_rows(k, index, "k"),
+                                                         _token_rows(v, index, "v"))
     n_seqs = cu_seqlens.shape[0] - 1
-    (q_ptr, q_step), (k_ptr, k_step), (v_ptr, v_step) = _token_rows(q, "q"), _token_rows(k, "k"), _token_rows(v, "v")
-    with _on(q.device, stream) as st:
-        if out is None:
-            out = _made((T, hq, d), q.dtype, q.device, stream)
-        elif out.shape != q.shape or out.dtype != q.dtype:
-            raise ValueError("out must have q's shape and dtype")
-        if lse is None and want_lse:
-            lse = _made((T, hq), torch.float32, q.device, stream)
-        elif lse is not None and (tuple(lse.shape) != (T, hq) or lse.dtype != torch.float32):
-            raise ValueError("lse must be float32 [T, n_q_heads]")
-        _check(_lib.sq_prompt_attention(q_ptr, q_step, k_ptr, k_step, v_ptr, v_step,
-                                        _i32(cu_seqlens, (n_seqs + 1,), "cu_seqlens"), n_seqs, T, hq, k.shape[1], d,
-                                        float(d ** -0.5 if scale is None else scale), int(causal), _dev(out, "out"),
-                                        _opt_dev(lse, "lse"), st), "sq_prompt_attention")
+    out, o_ptr = _given_or_made(out, q, shape, torch.bfloat16, index, stream, "out")
+    l_ptr = None
+    if lse is not None or want_lse:
+        lse, l_ptr = _given_or_made(lse, q, (T, hq), torch.float32, index, stream, "lse")
+    _launch(index, stream, "sq_prompt_attention", q_ptr, q_step, k_ptr, k_step, v_ptr, v_step,
+            _shaped(cu_seqlens, (n_seqs + 1,), torch.int32, index, "cu_seqlens"), n_seqs, T, hq, heads, d,
+            d ** -0.5 if scale is None else scale, 1 if causal else 0, o_ptr, l_ptr)
     return out if lse is None else (out, lse)
 
 
