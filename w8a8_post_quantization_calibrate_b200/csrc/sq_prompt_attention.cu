@@ -35,7 +35,7 @@ struct PromptArgs {
 //   Warps 0-3 and 4-7: softmax and results of the two tiles. Warp 8 loads (TMA: Q, and K
 // and V tiles of 128 tokens in a ring), warp 9 issues the products.
 constexpr int kPThreads = 384;
-constexpr int kPSlots = 4;              // ring slots, each a K or a V tile
+constexpr int kPSlots = 5;              // ring slots, each a K or a V tile
 // registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
 constexpr int kPSoftRegs = 224, kPOtherRegs = 56;
 constexpr float kPSlack = 8.0f;
@@ -48,18 +48,29 @@ struct PromptSmem {
     static constexpr int TOTAL = 1024 + 2 * TILE + kPSlots * TILE;
 };
 
-// O += P V with P in tensor memory.
-__device__ __forceinline__ void mma_bf16_ta(uint32_t d_tmem, uint32_t a_tmem, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\t"
-                 "setp.ne.b32 p, %4, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}"
-                 :: "r"(d_tmem), "r"(a_tmem), "l"(bdesc), "r"(idesc), "r"(accumulate)
-                 : "memory");
+// The products' operands by the low words of their shared-memory descriptors (address and
+// leading offset; the high word is the same for every tile here: 8-row groups 1024 bytes
+// apart, version 1, 128-byte swizzle). The low words are sums of warp-uniform
+// 32-bit values: building whole descriptors in the issuing thread took 80 to 110 cycles a
+// product, more than the 64 that one needs on the tensor cores.
+constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
+// Tiles whose rows run along the contraction (leading offset unused, 1), and tiles
+// whose rows ARE the contraction (the next 64 columns a box further).
+__device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, uint32_t leading) { return ((smem_addr & 0x3FFFFu) >> 4) | (leading << 16); }
+template <bool FIRST>
+__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+                 "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(FIRST ? 0 : 1) : "memory");
 }
-// A tile whose rows are the contraction: 128-byte swizzled rows of 64 columns, groups of 8
-// rows 1024 bytes apart (stride offset), the next 64 columns a box further (leading offset).
-__device__ __forceinline__ uint64_t make_sw128_rows_desc(uint32_t smem_addr, uint32_t box_bytes) {
-    return make_sw128_kmajor_desc(smem_addr) - ((uint64_t)1 << 16) + ((uint64_t)(box_bytes >> 4) << 16);
+__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
+    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+                 "mov.b64 db, {%2, %4};\n\t"
+                 "setp.ne.b32 p, %5, 0;\n\t"
+                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate) : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -145,7 +156,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
-    const uint32_t tmem = tmem_base_s;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, tmem_base_s, 0);
     const uint32_t t_s = tmem, t_o = tmem + 256;   // scores at 0, 128; accumulators at 256, 256 + D
     const long long limit = g.wait_limit;
     volatile int* abort = &abort_flag;
@@ -217,13 +228,17 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 }
                 return (bool)__all_sync(0xffffffffu, there);
             };
+            const uint32_t q_low = desc_low(base, 1), k_low = desc_low(base + S::RING, 1), v_low = desc_low(base + S::RING, S::BOX >> 4);
+            constexpr uint32_t STEP = S::TILE >> 4;
             auto scores = [&](int i) {   // S_i = Q_i K^T from k_slot
-                if (lane != 0) return;
+                const uint32_t a = q_low + i * STEP, b = k_low + k_slot * STEP, d = t_s + 128 * i;
+                if (lane == 0) {
+                    mma_ss<true>(d, a, b, IS);
 #pragma unroll
-                for (int k = 0; k < D / 16; ++k)
-                    mma_bf16(t_s + 128 * i, make_sw128_kmajor_desc(base + i * S::TILE + (k >> 2) * S::BOX + (k & 3) * 32),
-                             make_sw128_kmajor_desc(base + S::RING + k_slot * S::TILE + (k >> 2) * S::BOX + (k & 3) * 32), IS, k > 0);
-                mma_commit(s_full + 8 * i);
+                    for (int k = 1; k < D / 16; ++k)
+                        mma_ss<false>(d, a + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), b + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), IS);
+                    mma_commit(s_full + 8 * i);
+                }
             };
             for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x, ++work) {
                 const int n = max(w.n[0], w.n[1]);
@@ -248,7 +263,6 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                         asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
                         __syncwarp();
                     }
-                    if (j + 1 < n) ok = take(k_slot);
                     for (int i = 0; ok && i < 2; ++i) {
                         if (j < w.n[i]) {
                             // the weights are there; on a new item this also says that the same
@@ -257,15 +271,17 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                             if (!ok) break;
                             ++p_turn[i];
                             tc_fence_after();
+                            const uint32_t d = t_o + D * i, a = t_s + 128 * i, b = v_low + v_slot * STEP;
                             if (lane == 0) {
+                                mma_ts(d, a, b, IO, j > 0);
 #pragma unroll
-                                for (int k = 0; k < 8; ++k)
-                                    mma_bf16_ta(t_o + D * i, t_s + 128 * i + 8 * k,
-                                                make_sw128_rows_desc(base + S::RING + v_slot * S::TILE + k * 2048, S::BOX), IO, j > 0 || k > 0);
+                                for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, b + k * (2048 >> 4), IO, 1);
                                 if (j + 1 == w.n[i]) mma_commit(o_full + 8 * i);
                             }
                         }
                         if (i == 1 && lane == 0) mma_commit(empty + 8 * v_slot);
+                        if (i == 0 && j + 1 < n) ok = take(k_slot);
+                        if (!ok) break;
                         if (j + 1 < w.n[i]) scores(i);
                     }
                     if (ok && j + 1 < n && lane == 0) {
