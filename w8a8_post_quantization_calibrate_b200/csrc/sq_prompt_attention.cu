@@ -32,10 +32,10 @@ struct PromptArgs {
 // above it (any row of the warp), so the accumulator is rarely rescaled: P is at most 2^8,
 // and sums and accumulators in fp32 do not care. P is rounded to bf16 (relative
 // 2^-8 at most) because the product takes two bf16 operands.
-//   Warps 0-3 and 4-7: softmax and results of the two tiles. Warp 8 loads (TMA: Q, and K
-// and V tiles of 128 tokens in a ring), warp 9 issues the products.
+//   Warp 0 loads (TMA: Q, and K and V tiles of 128 tokens), warp 1 issues the products.
+// Warps 4-7 and 8-11: softmax and results of the two tiles.
 constexpr int kPThreads = 384;
-constexpr int kPSlots = 5;              // ring slots, each a K or a V tile
+constexpr int kPSlots = 4;              // tiles in flight: K, V, K, V; key tile number c is in slots 2 (c & 1) and 2 (c & 1) + 1
 // registers a thread: 168 at launch times 12 warps are as many as 224 times 8 and 56 times 4
 constexpr int kPSoftRegs = 224, kPOtherRegs = 56;
 constexpr float kPSlack = 8.0f;
@@ -50,27 +50,36 @@ struct PromptSmem {
 
 // The products' operands by the low words of their shared-memory descriptors (address and
 // leading offset; the high word is the same for every tile here: 8-row groups 1024 bytes
-// apart, version 1, 128-byte swizzle). The low words are sums of warp-uniform
-// 32-bit values: building whole descriptors in the issuing thread took 80 to 110 cycles a
-// product, more than the 64 that one needs on the tensor cores.
+// apart, version 1, 128-byte swizzle). A product takes 64 cycles on the tensor cores, and
+// the issuing warp has to keep that pace: with a slot's address worked out for every
+// product it took 80 to 120, and two long prompts 735 us. So a step over a key tile is
+// compiled twice, for the two places a tile can have, and its operands are constants.
 constexpr uint32_t kDescHigh = (1024u >> 4) | (1u << 14) | (2u << 29);
 // Tiles whose rows run along the contraction (leading offset unused, 1), and tiles
 // whose rows ARE the contraction (the next 64 columns a box further).
 __device__ __forceinline__ uint32_t desc_low(uint32_t smem_addr, uint32_t leading) { return ((smem_addr & 0x3FFFFu) >> 4) | (leading << 16); }
-template <bool FIRST>
-__device__ __forceinline__ void mma_ss(uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 da, db;\n\t"
+// All lanes call these with the same operands and `lead` says which one issues: no branch
+// around them, so that the operands stay in uniform registers.
+template <int ACCUMULATE>
+__device__ __forceinline__ void mma_ss(uint32_t lead, uint32_t d_tmem, uint32_t a_low, uint32_t b_low, uint32_t idesc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 da, db;\n\t"
                  "mov.b64 da, {%1, %4};\n\tmov.b64 db, {%2, %4};\n\t"
-                 "setp.ne.b32 p, %5, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
-                 :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(FIRST ? 0 : 1) : "memory");
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], da, db, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_low), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(ACCUMULATE), "r"(lead) : "memory");
 }
-__device__ __forceinline__ void mma_ts(uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc, uint32_t accumulate) {
-    asm volatile("{\n\t.reg .pred p;\n\t.reg .b64 db;\n\t"
+template <int ACCUMULATE>
+__device__ __forceinline__ void mma_ts(uint32_t lead, uint32_t d_tmem, uint32_t a_tmem, uint32_t b_low, uint32_t idesc) {
+    asm volatile("{\n\t.reg .pred p, q;\n\t.reg .b64 db;\n\t"
                  "mov.b64 db, {%2, %4};\n\t"
-                 "setp.ne.b32 p, %5, 0;\n\t"
-                 "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
-                 :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "n"(kDescHigh), "r"(accumulate) : "memory");
+                 "setp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\t"
+                 "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], db, %3, p;\n\t}"
+                 :: "r"(d_tmem), "r"(a_tmem), "r"(b_low), "r"(idesc), "n"(kDescHigh), "n"(ACCUMULATE), "r"(lead) : "memory");
+}
+__device__ __forceinline__ void commit_if(uint32_t lead, uint32_t bar) {
+    asm volatile("{\n\t.reg .pred q;\n\tsetp.ne.b32 q, %1, 0;\n\t"
+                 "@q tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];\n\t}"
+                 :: "r"(bar), "r"(lead) : "memory");
 }
 __device__ __forceinline__ void tmem_st_32x32b_x32(uint32_t taddr, const uint32_t* r) {
     asm volatile(
@@ -90,12 +99,22 @@ __device__ __forceinline__ uint64_t pair_fma(uint64_t a, uint64_t b, uint64_t c)
     return r;
 }
 
+// A wait of a whole warp.
+__device__ __forceinline__ bool warp_wait(uint32_t bar, uint32_t parity, long long limit, volatile int* abort, unsigned int site) {
+    return __all_sync(0xffffffffu, mbar_wait(bar, parity, limit, abort, site));
+}
+
+template <uint32_t V>
+struct Const {
+    static constexpr uint32_t v = V;
+};
+
 // Work items in order: every role walks them alike.
 struct PromptWalk {
     int64_t f0 = 0;        // blocks of the sequences before b
     int b = -1, start = 0, len = 0, nb = 0;
     int h, row;            // head; first query row, in the sequence
-    int n[2];              // key tiles of the two query tiles
+    int n0, n1;            // key tiles of the two query tiles, n0 <= n1 unless n1 is 0
     __device__ __forceinline__ bool find(const PromptArgs& g, int64_t id) {
         const int64_t f = id / g.n_q_heads;
         h = (int)(id % g.n_q_heads);
@@ -108,11 +127,8 @@ struct PromptWalk {
             nb = (len + 255) / 256;
         }
         row = (nb - 1 - (int)(f - f0)) * 256;
-#pragma unroll
-        for (int i = 0; i < 2; ++i) {
-            const int r = row + 128 * i;
-            n[i] = r >= len ? 0 : (min(len, g.causal ? r + 128 : len) + 127) / 128;
-        }
+        n0 = (min(len, g.causal ? row + 128 : len) + 127) / 128;
+        n1 = row + 128 >= len ? 0 : (min(len, g.causal ? row + 256 : len) + 127) / 128;
         return true;
     }
 };
@@ -127,7 +143,8 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     __shared__ __align__(8) uint64_t bars[2 + 2 * kPSlots + 6 + 1];
     __shared__ uint32_t tmem_base_s;
     __shared__ int abort_flag, drain_flag;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    __shared__ uint32_t sent[kPSlots];   // loads into each slot
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);   // uniform to the compiler
     const uint32_t base = (smem_u32(smem_raw) + 1023u) & ~1023u;
     uint8_t* base_ptr = smem_raw + (base - smem_u32(smem_raw));
     const uint32_t q_full = smem_u32(bars), q_empty = q_full + 8, full = q_full + 16, empty = full + 8 * kPSlots;
@@ -138,6 +155,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         for (int i = 0; i < kPSlots; ++i) {
             mbar_init(full + 8 * i, 1);
             mbar_init(empty + 8 * i, 1);
+            sent[i] = 0;
         }
         for (int i = 0; i < 2; ++i) {
             mbar_init(s_full + 8 * i, 1);
@@ -152,7 +170,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         tma_prefetch_desc(&map_k);
         tma_prefetch_desc(&map_v);
     }
-    if (warp == 9) tmem_alloc<512>(smem_u32(&tmem_base_s));
+    if (warp == 1) tmem_alloc<512>(smem_u32(&tmem_base_s));
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -164,131 +182,136 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     pdl_trigger();
     PromptWalk w;
 
-    if (warp >= 8) {
+    if (warp < 4) {
         asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" :: "n"(kPOtherRegs));
-        if (warp == 8) {
+        if (warp == 0) {
             // ------------------------------------------------------------ loads
             if (lane == 0) {
-                int slot = 0, work = 0;
-                uint32_t turn = 0;
-                int64_t issued = 0;
+                int work = 0;
+                uint32_t count = 0;   // key tiles sent
                 bool ok = true;
                 if (blockIdx.x == 0)   // once: offsets that the walk cuts
                     for (int b = 0; b <= g.n_seqs; ++b) {
                         const int64_t a = __ldg(g.cu + b);
                         if (a < 0 || a > g.T || (b > 0 && a < __ldg(g.cu + b - 1))) { record_status(SQ_ERR_BOUNDS, SITE_PROMPT); break; }
                     }
-                auto send = [&](const CUtensorMap* map, int h, int tok) {
+                auto send = [&](const CUtensorMap* map, int slot, int h, int tok) {
+                    const uint32_t turn = count >> 1;
                     if (turn > 0 && !mbar_wait(empty + 8 * slot, (turn - 1) & 1, limit, abort, SITE_PROMPT_WAIT)) return false;
                     mbar_arrive_expect_tx(full + 8 * slot, S::TILE);
 #pragma unroll
                     for (int c = 0; c < NBOX; ++c)
                         tma_load_3d(base + S::RING + slot * S::TILE + c * S::BOX, map, full + 8 * slot, 64 * c, h, tok);
-                    ++issued;
-                    if (++slot == kPSlots) {
-                        slot = 0;
-                        ++turn;
-                    }
+                    sent[slot] = turn + 1;
                     return true;
                 };
                 for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x, ++work) {
                     if (work > 0 && !mbar_wait(q_empty, (work - 1) & 1, limit, abort, SITE_PROMPT_WAIT)) break;
-                    const int tiles = w.n[1] > 0 ? 2 : 1;
+                    const int tiles = w.n1 > 0 ? 2 : 1;
                     mbar_arrive_expect_tx(q_full, tiles * S::TILE);
                     for (int i = 0; i < tiles; ++i)
 #pragma unroll
                         for (int c = 0; c < NBOX; ++c)
                             tma_load_3d(base + i * S::TILE + c * S::BOX, &map_q, q_full, 64 * c, w.h, w.start + w.row + 128 * i);
-                    const int n = max(w.n[0], w.n[1]), hk = w.h / g.group;
-                    for (int j = 0; ok && j < n; ++j) ok = send(&map_k, hk, w.start + 128 * j) && send(&map_v, hk, w.start + 128 * j);
+                    const int n = max(w.n0, w.n1), hk = w.h / g.group;
+                    for (int j = 0; ok && j < n; ++j, ++count)
+                        ok = send(&map_k, 2 * (count & 1), hk, w.start + 128 * j) && send(&map_v, 2 * (count & 1) + 1, hk, w.start + 128 * j);
                 }
                 if (*abort) {   // a wait ran out: the copies in flight end before the shared memory goes
                     volatile int* drain = &drain_flag;
-                    for (int64_t i = issued > kPSlots ? issued - kPSlots : 0; i < issued; ++i)
-                        mbar_wait(full + 8 * (int)(i % kPSlots), (i / kPSlots) & 1, limit, drain, SITE_PROMPT_WAIT);
-                    if (work > 0 || issued > 0) mbar_wait(q_full, (work - 1) & 1, limit, drain, SITE_PROMPT_WAIT);
+                    for (int i = 0; i < kPSlots; ++i)
+                        if (sent[i] > 0) mbar_wait(full + 8 * i, (sent[i] - 1) & 1, limit, drain, SITE_PROMPT_WAIT);
+                    if (work > 0) mbar_wait(q_full, (work - 1) & 1, limit, drain, SITE_PROMPT_WAIT);
                 }
             }
             __syncwarp();
-        } else if (warp == 9) {
+        } else if (warp == 1) {
             // ------------------------------------------------------------ products
             constexpr uint32_t IS = make_idesc_bf16(128, 128);
             constexpr uint32_t IO = make_idesc_bf16(128, D) | (1u << 16);   // V's rows are the contraction
-            int slot = 0, work = 0;
-            uint32_t turn = 0;
-            uint32_t p_turn[2] = {0, 0};
-            bool ok = true;
-            int k_slot = 0, v_slot = 0;
-            auto take = [&](int& at) {   // the next ring slot, once it is there
-                at = slot;
-                const bool there = mbar_wait(full + 8 * slot, turn & 1, limit, abort, SITE_PROMPT_WAIT);
-                if (++slot == kPSlots) {
-                    slot = 0;
-                    ++turn;
-                }
-                return (bool)__all_sync(0xffffffffu, there);
-            };
+            // All 512 columns are this CTA's, so its tensor memory begins at address 0.
+            constexpr uint32_t TS = 0, TO = 256;
+            int work = 0;
+            uint32_t count = 0, p_turn0 = 0, p_turn1 = 0;   // key tiles begun; weights taken
+            const uint32_t lead = lane == 0;
             const uint32_t q_low = desc_low(base, 1), k_low = desc_low(base + S::RING, 1), v_low = desc_low(base + S::RING, S::BOX >> 4);
             constexpr uint32_t STEP = S::TILE >> 4;
-            auto scores = [&](int i) {   // S_i = Q_i K^T from k_slot
-                const uint32_t a = q_low + i * STEP, b = k_low + k_slot * STEP, d = t_s + 128 * i;
-                if (lane == 0) {
-                    mma_ss<true>(d, a, b, IS);
-#pragma unroll
-                    for (int k = 1; k < D / 16; ++k)
-                        mma_ss<false>(d, a + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), b + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), IS);
-                    mma_commit(s_full + 8 * i);
-                }
+            auto wait = [&](uint32_t bar, uint32_t parity) {
+                return warp_wait(bar, parity, limit, abort, SITE_PROMPT_WAIT);
             };
-            for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x, ++work) {
-                const int n = max(w.n[0], w.n[1]);
-                ok = __all_sync(0xffffffffu, mbar_wait(q_full, work & 1, limit, abort, SITE_PROMPT_WAIT)) && take(k_slot);
-                if (!ok) break;
+            // S_i = Q_i K^T from K slot 2 P
+            auto scores = [&](auto I_, auto P_) {
+                constexpr uint32_t I = decltype(I_)::v, P = decltype(P_)::v;
+                const uint32_t a = q_low + I * STEP, b = k_low + 2 * P * STEP;
+                mma_ss<0>(lead, TS + 128 * I, a, b, IS);
+#pragma unroll
+                for (int k = 1; k < D / 16; ++k)
+                    mma_ss<1>(lead, TS + 128 * I, a + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), b + (((k >> 2) * S::BOX + (k & 3) * 32) >> 4), IS);
+                commit_if(lead, s_full + 8 * I);
+            };
+            // O_i += P_i V from V slot 2 P + 1, once the weights are there; on a new item that also
+            // says that the same warps have read the last one's accumulator.
+            auto outputs = [&](auto I_, auto P_, uint32_t& p_turn, bool first, bool last) {
+                constexpr uint32_t I = decltype(I_)::v, P = decltype(P_)::v;
+                if (!wait(p_full + 8 * I, p_turn & 1)) return false;
+                ++p_turn;
                 tc_fence_after();
-                scores(0);
-                if (w.n[1] > 0) scores(1);
-                if (lane == 0) {
-                    mma_commit(empty + 8 * k_slot);
-                    if (n == 1) mma_commit(q_empty);
-                }
-                for (int j = 0; ok && j < n; ++j) {
-                    ok = take(v_slot);
-                    if (!ok) break;
-                    const int rows = w.len - 128 * j;
-                    if (rows < 128) {   // rows behind the sequence: a weight of 0 times what lies there must be 0
-                        uint8_t* v = base_ptr + S::RING + v_slot * S::TILE;
-                        for (int u = rows * 8 + lane; u < 128 * 8; u += 32)
+                const uint32_t b = v_low + (2 * P + 1) * STEP;
+                if (first) mma_ts<0>(lead, TO + D * I, TS + 128 * I, b, IO);
+                else mma_ts<1>(lead, TO + D * I, TS + 128 * I, b, IO);
 #pragma unroll
-                            for (int c = 0; c < NBOX; ++c) *reinterpret_cast<uint4*>(v + c * S::BOX + u * 16) = make_uint4(0, 0, 0, 0);
-                        asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
-                        __syncwarp();
-                    }
-                    for (int i = 0; ok && i < 2; ++i) {
-                        if (j < w.n[i]) {
-                            // the weights are there; on a new item this also says that the same
-                            // warps have read the last one's accumulator
-                            ok = __all_sync(0xffffffffu, mbar_wait(p_full + 8 * i, p_turn[i] & 1, limit, abort, SITE_PROMPT_WAIT));
-                            if (!ok) break;
-                            ++p_turn[i];
-                            tc_fence_after();
-                            const uint32_t d = t_o + D * i, a = t_s + 128 * i, b = v_low + v_slot * STEP;
-                            if (lane == 0) {
-                                mma_ts(d, a, b, IO, j > 0);
+                for (int k = 1; k < 8; ++k) mma_ts<1>(lead, TO + D * I, TS + 128 * I + 8 * k, b + k * (2048 >> 4), IO);
+                if (last) commit_if(lead, o_full + 8 * I);
+                return true;
+            };
+            constexpr Const<0> c0{};
+            constexpr Const<1> c1{};
+            int n0 = 0, n1 = 0, len = 0;   // of the item, uniform to the compiler
+            // Key tile j, in the slots of P; the next one's are those of N.
+            auto step = [&](auto P_, auto N_, int j, int n) {
+                constexpr uint32_t P = decltype(P_)::v, N = decltype(N_)::v;
+                if (!wait(full + 8 * (2 * P + 1), (count >> 1) & 1)) return false;
+                const int rows = len - 128 * j;
+                if (rows < 128) {   // rows behind the sequence: a weight of 0 times what lies there must be 0
+                    uint8_t* v = base_ptr + S::RING + (2 * P + 1) * S::TILE;
+                    for (int u = rows * 8 + lane; u < 128 * 8; u += 32)
 #pragma unroll
-                                for (int k = 1; k < 8; ++k) mma_ts(d, a + 8 * k, b + k * (2048 >> 4), IO, 1);
-                                if (j + 1 == w.n[i]) mma_commit(o_full + 8 * i);
-                            }
-                        }
-                        if (i == 1 && lane == 0) mma_commit(empty + 8 * v_slot);
-                        if (i == 0 && j + 1 < n) ok = take(k_slot);
-                        if (!ok) break;
-                        if (j + 1 < w.n[i]) scores(i);
-                    }
-                    if (ok && j + 1 < n && lane == 0) {
-                        mma_commit(empty + 8 * k_slot);
-                        if (j + 2 == n) mma_commit(q_empty);
-                    }
+                        for (int c = 0; c < NBOX; ++c) *reinterpret_cast<uint4*>(v + c * S::BOX + u * 16) = make_uint4(0, 0, 0, 0);
+                    asm volatile("fence.proxy.async.shared::cta;" ::: "memory");
+                    __syncwarp();
                 }
+                if (j < n0 && !outputs(c0, P_, p_turn0, j == 0, j + 1 == n0)) return false;
+                if (j + 1 < n) {
+                    if (!wait(full + 8 * 2 * N, ((count + 1) >> 1) & 1)) return false;
+                    if (j + 1 < n0) scores(c0, N_);
+                }
+                if (j < n1 && !outputs(c1, P_, p_turn1, j == 0, j + 1 == n1)) return false;
+                commit_if(lead, empty + 8 * (2 * P + 1));
+                if (j + 1 < n) {
+                    if (j + 1 < n1) scores(c1, N_);
+                    commit_if(lead, empty + 8 * 2 * N);
+                    if (j + 2 == n) commit_if(lead, q_empty);
+                }
+                ++count;
+                return true;
+            };
+            auto begin = [&](auto P_, int n) {
+                constexpr uint32_t P = decltype(P_)::v;
+                if (!wait(full + 8 * 2 * P, (count >> 1) & 1)) return false;
+                scores(c0, P_);
+                if (n1 > 0) scores(c1, P_);
+                commit_if(lead, empty + 8 * 2 * P);
+                if (n == 1) commit_if(lead, q_empty);
+                return true;
+            };
+            bool ok = true;
+            for (int64_t id = blockIdx.x; ok && __all_sync(0xffffffffu, w.find(g, id)); id += gridDim.x, ++work) {
+                n0 = __shfl_sync(0xffffffffu, w.n0, 0);
+                n1 = __shfl_sync(0xffffffffu, w.n1, 0);
+                len = __shfl_sync(0xffffffffu, w.len, 0);
+                const int n = max(n0, n1);
+                ok = wait(q_full, work & 1) && ((count & 1) ? begin(c1, n) : begin(c0, n));
+                for (int j = 0; ok && j < n; ++j) ok = (count & 1) ? step(c1, c0, j, n) : step(c0, c1, j, n);
             }
             if (*abort) {   // products in flight end before the tensor memory goes
                 if (lane == 0) {
@@ -302,7 +325,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     } else {
         // ---------------------------------------------------------------- softmax
         asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kPSoftRegs));
-        const int i = warp >> 2;
+        const int i = (warp >> 2) - 1;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;   // this warp's 32 lanes of tensor memory
         const uint32_t ts = t_s + 128 * i + lanes, to = t_o + D * i + lanes;
         const float sc = g.scale;
@@ -310,14 +333,14 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
         uint32_t s_turn = 0, o_turn = 0;
         bool ok = true;
         for (int64_t id = blockIdx.x; ok && w.find(g, id); id += gridDim.x) {
-            const int n = w.n[i];
+            const int n = i == 0 ? w.n0 : w.n1;
             if (n == 0) continue;
             const int r = w.row + 128 * i + (tid & 127);      // this thread's row, in the sequence
             const int see = g.causal ? min(r + 1, w.len) : w.len;
             const int sure = g.causal ? min(w.row + 128 * i + 1, w.len) : w.len;   // what every row of the tile sees
             float m = kNoReference, l = 0.0f;
             for (int j = 0; j < n; ++j) {
-                ok = __all_sync(0xffffffffu, mbar_wait(s_full + 8 * i, s_turn & 1, limit, abort, SITE_PROMPT_WAIT));
+                ok = warp_wait(s_full + 8 * i, s_turn & 1, limit, abort, SITE_PROMPT_WAIT);
                 if (!ok) break;
                 ++s_turn;
                 tc_fence_after();
@@ -396,7 +419,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 l += a + b;
             }
             if (!ok) break;
-            ok = __all_sync(0xffffffffu, mbar_wait(o_full + 8 * i, o_turn & 1, limit, abort, SITE_PROMPT_WAIT));
+            ok = warp_wait(o_full + 8 * i, o_turn & 1, limit, abort, SITE_PROMPT_WAIT);
             if (!ok) break;
             ++o_turn;
             tc_fence_after();
@@ -425,7 +448,7 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
     }
     tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 1) {
         tc_fence_after();
         tmem_dealloc<512>(tmem);
     }
