@@ -118,6 +118,27 @@ template <> struct Chunk<float> {
     }
 };
 
+// The same 8 channels as they lie in memory, so that loads can be far ahead of their use.
+template <typename T> struct RawEight {
+    uint4 v[sizeof(T) / 2];
+    __device__ __forceinline__ void load(const T* p) {
+#pragma unroll
+        for (int i = 0; i < (int)sizeof(T) / 2; ++i) v[i] = reinterpret_cast<const uint4*>(p)[i];
+    }
+    __device__ __forceinline__ void get(float (&x)[8]) const {
+        if constexpr (sizeof(T) == 2) {
+            x[0] = bf16_lo(v[0].x); x[1] = bf16_hi(v[0].x); x[2] = bf16_lo(v[0].y); x[3] = bf16_hi(v[0].y);
+            x[4] = bf16_lo(v[0].z); x[5] = bf16_hi(v[0].z); x[6] = bf16_lo(v[0].w); x[7] = bf16_hi(v[0].w);
+        } else {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                x[4 * i] = __uint_as_float(v[i].x); x[4 * i + 1] = __uint_as_float(v[i].y);
+                x[4 * i + 2] = __uint_as_float(v[i].z); x[4 * i + 3] = __uint_as_float(v[i].w);
+            }
+        }
+    }
+};
+
 // Lane c of a head's head_dim / 16 lanes holds two chunks of 8 channels: for
 // c < rot/16 the chunks c and c + rot/16, which hold each other's partners in the
 // half layout (and whole pairs in the interleaved one); the other lanes hold
@@ -163,12 +184,30 @@ __device__ __forceinline__ uint32_t code_of(float x, float s) {
     const int q = __float2int_rn(__fdiv_rn(x, s));
     return (uint32_t)max(-127, min(127, q)) & 0xffu;
 }
+// clamp(round(RN(x / s))) of 8 values. x RN(1 / s) is within 3 2^-24 of RN(x / s) relatively,
+// so below 3e-5 for the |x / s| <= 127.5 that occur here; a value within 2^-13 of a half
+// integer is divided, the others cannot round differently. 1.5 2^23 added and
+// taken away rounds to the nearest integer, ties to even, and leaves the code in the
+// sum's low byte. A scale below 2^-100 (reciprocals near the top of fp32's range,
+// quotients that may pass 127) takes the divisions and the clamp.
 __device__ __forceinline__ uint2 codes_of(const float (&x)[8], float s) {
     if (!(s > 0.0f)) return make_uint2(0u, 0u);
     uint32_t t[8];
+    const float r = __frcp_rn(s);
+    bool near = !(s >= 7.888609052210118e-31f);
 #pragma unroll
-    for (int i = 0; i < 8; ++i) t[i] = code_of(x[i], s);
-    return make_uint2(t[0] | t[1] << 8 | t[2] << 16 | t[3] << 24, t[4] | t[5] << 8 | t[6] << 16 | t[7] << 24);
+    for (int i = 0; i < 8; ++i) {
+        const float q = __fmul_rn(x[i], r);
+        const float m = __fadd_rn(q, 12582912.0f);
+        t[i] = __float_as_uint(m);
+        near |= !(fabsf(__fsub_rn(q, __fsub_rn(m, 12582912.0f))) < 0.5f - 1.220703125e-4f);
+    }
+    if (near) {
+#pragma unroll
+        for (int i = 0; i < 8; ++i) t[i] = code_of(x[i], s);
+    }
+    return make_uint2(__byte_perm(__byte_perm(t[0], t[1], 0x0040), __byte_perm(t[2], t[3], 0x0040), 0x5410),
+                      __byte_perm(__byte_perm(t[4], t[5], 0x0040), __byte_perm(t[6], t[7], 0x0040), 0x5410));
 }
 __device__ __forceinline__ float code_at(uint32_t w, int i) { return (float)(int8_t)(w >> (8 * i)); }
 __device__ __forceinline__ uint2 requantize(uint2 w, float was, float s) {
@@ -182,19 +221,24 @@ __device__ __forceinline__ uint2 requantize(uint2 w, float was, float s) {
 }
 
 // ================================================================== rotary table
-constexpr int kTableRun = 32;   // positions that one thread walks
-
+// A thread has one frequency and RUN positions in a row: it works out the first angle's
+// cosine and sine and those of one step, and turns by the step from position to
+// position, z' = z (cos w + i sin w): four fp64 products an entry in place of a sincos. Each
+// turn adds at most some 2^-52, so 32 of them stay far below the one rounding to fp32
+// (2^-24). Longer runs amortise the two sincos and the power, shorter ones fill the GPU:
+// 131,072 positions x 64 frequencies took 32 us with a sincos for every entry.
 struct RopeFreq {
     double theta, factor, low, high, orig, magnitude;
 };
 
+template <int RUN>
 __global__ void __launch_bounds__(256)
 rope_table_kernel(float2* __restrict__ table, int64_t first, int64_t n_pos, int half, RopeFreq f) {
     pdl_wait();
     pdl_trigger();
     const int64_t id = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
     const int i = (int)(id % half);
-    const int64_t p0 = id / half * kTableRun;
+    const int64_t p0 = id / half * RUN;
     if (p0 >= n_pos) return;
     double w = pow(f.theta, -(double)i / (double)half);
     if (f.high > 0.0) {
@@ -204,11 +248,18 @@ rope_table_kernel(float2* __restrict__ table, int64_t first, int64_t n_pos, int 
     } else {
         w = w / f.factor;
     }
-    const int64_t end = min(n_pos, p0 + kTableRun);
-    for (int64_t p = p0; p < end; ++p) {
-        double s, c;
-        sincos((double)(first + p) * w, &s, &c);
-        table[p * half + i] = make_float2((float)(c * f.magnitude), (float)(s * f.magnitude));
+    double s, c, ds, dc;
+    sincos((double)(first + p0) * w, &s, &c);
+    sincos(w, &ds, &dc);
+    s *= f.magnitude;
+    c *= f.magnitude;
+    const int n = (int)min((int64_t)RUN, n_pos - p0);
+    float2* out = table + p0 * half + i;
+    for (int k = 0; k < n; ++k) {
+        out[(int64_t)k * half] = make_float2((float)c, (float)s);
+        const double t = c * dc - s * ds;
+        s = s * dc + c * ds;
+        c = t;
     }
 }
 
@@ -229,7 +280,7 @@ struct AppendArgs {
 };
 
 constexpr int kAppendThreads = 256;
-constexpr int kQHeads = 8;   // query heads of one block
+constexpr int kQRows = 128;   // (position, query head) rows of one block: 8 heads of 16 positions .. 1 of 128
 
 // NP passes of 128 / (D / 16) rows cover a span; K and V have 128 threads each.
 template <typename T, int D, int NP>
@@ -261,29 +312,42 @@ rope_append_kernel(const AppendArgs g) {
     const int64_t base = max((int64_t)0, ctx);
 
     if ((int)blockIdx.y >= g.c.n_heads) {   // ---- query heads
-        const int h0 = ((int)blockIdx.y - g.c.n_heads) * kQHeads;
-        const int nh = min(kQHeads, g.n_q_heads - h0);
+        const int per = kQRows >> sh;
+        const int h0 = ((int)blockIdx.y - g.c.n_heads) * per;
+        const int nh = min(per, g.n_q_heads - h0);
         const int rows = (int)(hi - lo) * nh;
         const int c = threadIdx.x % LPR;
         int ca, cb;
         lane_chunks(c, g.rot, ca, cb);
-        for (int r = threadIdx.x / LPR; r < rows; r += kAppendThreads / LPR) {
-            const int64_t p = lo + r / nh;
-            const int64_t t = t0 + p - base;
-            const int h = h0 + r % nh;
-            const T* x = static_cast<const T*>(g.q) + t * g.q_stride + (int64_t)h * D;
-            T* y = static_cast<T*>(g.q_out) + (t * g.n_q_heads + h) * D;
-            float xa[8], xb[8];
-            Chunk<T>::load(x + 8 * ca, xa);
-            Chunk<T>::load(x + 8 * cb, xb);
-            if (p < ok) {
-                rotate_lane(xa, xb, g.table + p * g.rot, c, g.rot, g.pairs);
-            } else {
+        constexpr int Q = 4, STEP = kAppendThreads / LPR;   // rows in flight; rows apart
+        for (int r0 = threadIdx.x / LPR; r0 < rows; r0 += Q * STEP) {
+            RawEight<T> ra[Q], rb[Q];
 #pragma unroll
-                for (int i = 0; i < 8; ++i) xa[i] = xb[i] = __int_as_float(0x7fc00000);
+            for (int k = 0; k < Q; ++k) {
+                const int r = r0 + k * STEP;
+                if (r >= rows) break;
+                const T* x = static_cast<const T*>(g.q) + (t0 + lo - base + r / nh) * g.q_stride + (int64_t)(h0 + r % nh) * D;
+                ra[k].load(x + 8 * ca);
+                rb[k].load(x + 8 * cb);
             }
-            Chunk<T>::store(y + 8 * ca, xa);
-            Chunk<T>::store(y + 8 * cb, xb);
+#pragma unroll
+            for (int k = 0; k < Q; ++k) {
+                const int r = r0 + k * STEP;
+                if (r >= rows) break;
+                const int64_t p = lo + r / nh;
+                T* y = static_cast<T*>(g.q_out) + ((t0 + p - base) * g.n_q_heads + h0 + r % nh) * D;
+                float xa[8], xb[8];
+                ra[k].get(xa);
+                rb[k].get(xb);
+                if (p < ok) {
+                    rotate_lane(xa, xb, g.table + p * g.rot, c, g.rot, g.pairs);
+                } else {
+#pragma unroll
+                    for (int i = 0; i < 8; ++i) xa[i] = xb[i] = __int_as_float(0x7fc00000);
+                }
+                Chunk<T>::store(y + 8 * ca, xa);
+                Chunk<T>::store(y + 8 * cb, xb);
+            }
         }
         return;
     }
@@ -304,6 +368,18 @@ rope_append_kernel(const AppendArgs g) {
     int ca, cb;
     lane_chunks(c, is_v ? 0 : g.rot, ca, cb);
     const int span = 1 << sh;
+    RawEight<T> ra[NP], rb[NP];
+#pragma unroll
+    for (int s = 0; s < NP; ++s) {
+        const int r = s * RP + r0;
+        const int64_t p = span0 + r;
+        if (r < span && p >= lo && p < hi) {
+            const int64_t t = t0 + p - base;
+            const T* x = (is_v ? static_cast<const T*>(g.v) + t * g.v_stride : static_cast<const T*>(g.k) + t * g.k_stride) + (int64_t)h * D;
+            ra[s].load(x + 8 * ca);
+            rb[s].load(x + 8 * cb);
+        }
+    }
     float xa[NP][8], xb[NP][8];
 #pragma unroll
     for (int s = 0; s < NP; ++s) {
@@ -312,9 +388,8 @@ rope_append_kernel(const AppendArgs g) {
         float m = 0.0f;
         if (r < span && p >= lo && p < hi) {
             const int64_t t = t0 + p - base;
-            const T* x = (is_v ? static_cast<const T*>(g.v) + t * g.v_stride : static_cast<const T*>(g.k) + t * g.k_stride) + (int64_t)h * D;
-            Chunk<T>::load(x + 8 * ca, xa[s]);
-            Chunk<T>::load(x + 8 * cb, xb[s]);
+            ra[s].get(xa[s]);
+            rb[s].get(xb[s]);
             if (p < ok) {
                 if (!is_v) rotate_lane(xa[s], xb[s], g.table + p * g.rot, c, g.rot, g.pairs);
 #pragma unroll
@@ -462,9 +537,13 @@ sq_status rope_table_impl(float* table, int64_t first, int64_t n_pos, int64_t ro
     if (!table) { set_error("table: NULL pointer"); return SQ_ERR_INVALID_ARG; }
     if (!aligned16(table)) { set_error("table must be 16-byte aligned"); return SQ_ERR_UNSUPPORTED; }
     const int half = (int)(rot / 2);
-    const int64_t threads = (n_pos + kTableRun - 1) / kTableRun * half;
-    return launch_pdl("rope_table_kernel", rope_table_kernel, dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, 1,
-                      reinterpret_cast<float2*>(table), first, n_pos, half, f);
+    // Runs of 32 where they still fill the GPU's threads, else of 4.
+    const bool many = n_pos / 32 * half >= (int64_t)device_info().sm_count * 1024;
+    const int run = many ? 32 : 4;
+    const int64_t threads = (n_pos + run - 1) / run * half;
+    return launch_pdl("rope_table_kernel", many ? rope_table_kernel<32> : rope_table_kernel<4>,
+                      dim3((unsigned)((threads + 255) / 256)), dim3(256), 0, st, 1, reinterpret_cast<float2*>(table), first,
+                      n_pos, half, f);
 }
 
 sq_status rope_append_impl(const sq_kv_cache* cache, const int32_t* block_table, int64_t max_pages, const int32_t* ctx_len,
@@ -503,7 +582,7 @@ sq_status rope_append_impl(const sq_kv_cache* cache, const int32_t* block_table,
     g.q = q; g.k = k; g.v = v; g.q_out = q_out; g.k_out = k_out; g.table = table;
     const int span = cache->scale_block > 16 ? cache->scale_block : 16;
     g.span_shift = log2_of(span);
-    const dim3 grid((unsigned)(T / span + 2 * n_seqs), (unsigned)(cache->n_heads + (n_q_heads + kQHeads - 1) / kQHeads));
+    const dim3 grid((unsigned)(T / span + 2 * n_seqs), (unsigned)(cache->n_heads + (n_q_heads + kQRows / span - 1) / (kQRows / span)));
     if (dt == SQ_F32) return D == 64 ? launch_append<float, 64>(g, grid, st) : launch_append<float, 128>(g, grid, st);
     return D == 64 ? launch_append<__nv_bfloat16, 64>(g, grid, st) : launch_append<__nv_bfloat16, 128>(g, grid, st);
 }

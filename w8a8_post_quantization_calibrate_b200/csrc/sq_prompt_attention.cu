@@ -361,17 +361,17 @@ prompt_attention_kernel(const __grid_constant__ CUtensorMap map_q, const __grid_
                 if (neg) {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        t[c] = __uint_as_float(x[c][0]);
+                        t[c] = fminf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
 #pragma unroll
-                        for (int e = 1; e < 32; ++e) t[c] = fminf(t[c], __uint_as_float(x[c][e]));
+                        for (int e = 2; e < 32; e += 2) t[c] = fminf(t[c], fminf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
                     }
                     t[0] = fminf(fminf(t[0], t[1]), fminf(t[2], t[3]));
                 } else {
 #pragma unroll
                     for (int c = 0; c < 4; ++c) {
-                        t[c] = __uint_as_float(x[c][0]);
+                        t[c] = fmaxf(__uint_as_float(x[c][0]), __uint_as_float(x[c][1]));
 #pragma unroll
-                        for (int e = 1; e < 32; ++e) t[c] = fmaxf(t[c], __uint_as_float(x[c][e]));
+                        for (int e = 2; e < 32; e += 2) t[c] = fmaxf(t[c], fmaxf(__uint_as_float(x[c][e]), __uint_as_float(x[c][e + 1])));
                     }
                     t[0] = fmaxf(fmaxf(t[0], t[1]), fmaxf(t[2], t[3]));
                 }
