@@ -279,16 +279,19 @@ struct AppendArgs {
     const float* table;
 };
 
-constexpr int kAppendThreads = 256;
 constexpr int kQRows = 128;   // (position, query head) rows of one block: 8 heads of 16 positions .. 1 of 128
 
-// NP passes of 128 / (D / 16) rows cover a span; K and V have 128 threads each.
-template <typename T, int D, int NP>
-__global__ void __launch_bounds__(kAppendThreads)
+// A block has a span of one head of K or of V, or of some query heads; NP passes of
+// THREADS / (D / 16) rows cover the span. Small blocks, because a block is a chain of
+// dependent steps (its sequence, its rows, their maximum, the codes) that only
+// other blocks on the SM can hide: 1024 threads of 64 registers an SM take 62 us for five
+// prompts of 3,500 tokens and 32 heads, 512 of 126 took 81.
+template <typename T, int D, int THREADS, int NP>
+__global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 rope_append_kernel(const AppendArgs g) {
     constexpr int LPR = D / 16;          // lanes of a row
-    constexpr int RP = 128 / LPR;        // rows of a pass
-    __shared__ float row_max[2][128];
+    constexpr int RP = THREADS / LPR;    // rows of a pass
+    __shared__ float row_max[128];
     pdl_wait();
     pdl_trigger();
     const int64_t u = blockIdx.x;
@@ -311,15 +314,15 @@ rope_append_kernel(const AppendArgs g) {
     if (ok < hi && threadIdx.x == 0 && blockIdx.y == 0) record_status(SQ_ERR_BOUNDS, SITE_KV_APPEND);
     const int64_t base = max((int64_t)0, ctx);
 
-    if ((int)blockIdx.y >= g.c.n_heads) {   // ---- query heads
+    if ((int)blockIdx.y >= 2 * g.c.n_heads) {   // ---- query heads
         const int per = kQRows >> sh;
-        const int h0 = ((int)blockIdx.y - g.c.n_heads) * per;
+        const int h0 = ((int)blockIdx.y - 2 * g.c.n_heads) * per;
         const int nh = min(per, g.n_q_heads - h0);
         const int rows = (int)(hi - lo) * nh;
         const int c = threadIdx.x % LPR;
         int ca, cb;
         lane_chunks(c, g.rot, ca, cb);
-        constexpr int Q = 4, STEP = kAppendThreads / LPR;   // rows in flight; rows apart
+        constexpr int Q = 2, STEP = THREADS / LPR;   // rows in flight; rows apart
         for (int r0 = threadIdx.x / LPR; r0 < rows; r0 += Q * STEP) {
             RawEight<T> ra[Q], rb[Q];
 #pragma unroll
@@ -352,11 +355,11 @@ rope_append_kernel(const AppendArgs g) {
         return;
     }
 
-    // ---- one head of K (threads 0 .. 127) and of V
-    const int h = blockIdx.y;
-    const int is_v = threadIdx.x >> 7;
-    const int c = (threadIdx.x & 127) % LPR;
-    const int r0 = (threadIdx.x & 127) / LPR;
+    // ---- one head of K or of V
+    const bool is_v = (int)blockIdx.y >= g.c.n_heads;
+    const int h = (int)blockIdx.y - (is_v ? g.c.n_heads : 0);
+    const int c = threadIdx.x % LPR;
+    const int r0 = threadIdx.x / LPR;
     int64_t page = -1;
     if (lo < ok) {
         page = __ldg(g.block_table + b * g.max_pages + (span0 >> g.c.page_shift));
@@ -406,7 +409,7 @@ rope_append_kernel(const AppendArgs g) {
         }
 #pragma unroll
         for (int o = LPR / 2; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-        if (c == 0 && r < span) row_max[is_v][r] = m;
+        if (c == 0 && r < span) row_max[r] = m;
     }
     if (page < 0) return;   // the whole block
     const int bs = g.c.block_shift, block = 1 << bs;
@@ -430,7 +433,7 @@ rope_append_kernel(const AppendArgs g) {
         const int64_t first = span0 + g0;
         if (p >= ok || first + block <= lo) continue;   // nothing of this row, or of its block, is new
         float m = 0.0f;
-        for (int i = 0; i < block; ++i) m = fmaxf(m, row_max[is_v][g0 + i]);
+        for (int i = 0; i < block; ++i) m = fmaxf(m, row_max[g0 + i]);
         const float scale = fmaxf(was[s], __fdiv_rn(m, 127.0f));
         int8_t* row = codes + (int64_t)(slot0 + r) * D;
         if (p >= lo) {
@@ -503,12 +506,12 @@ sq_status check_kv_dtype(sq_dtype dt) {
 
 template <typename T, int D>
 sq_status launch_append(const AppendArgs& g, dim3 grid, cudaStream_t st) {
-    const int passes = ((1 << g.span_shift) + (2048 / D) - 1) / (2048 / D);   // 2048 / D = rows of a pass
-    const dim3 block(kAppendThreads);
-    if (passes <= 1) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 1>, grid, block, 0, st, 1, g);
-    if (passes <= 2) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 2>, grid, block, 0, st, 1, g);
-    if (passes <= 4) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 4>, grid, block, 0, st, 1, g);
-    return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 8>, grid, block, 0, st, 1, g);
+    constexpr int RP = 4096 / D;   // rows of a pass of 256 threads
+    const int span = 1 << g.span_shift;
+    if (span <= 2048 / D) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 128, 1>, grid, dim3(128), 0, st, 1, g);
+    if (span <= RP) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 1>, grid, dim3(256), 0, st, 1, g);
+    if (span <= 2 * RP) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 2>, grid, dim3(256), 0, st, 1, g);
+    return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 4>, grid, dim3(256), 0, st, 1, g);
 }
 
 sq_status rope_table_impl(float* table, int64_t first, int64_t n_pos, int64_t rot, double theta,
@@ -582,7 +585,7 @@ sq_status rope_append_impl(const sq_kv_cache* cache, const int32_t* block_table,
     g.q = q; g.k = k; g.v = v; g.q_out = q_out; g.k_out = k_out; g.table = table;
     const int span = cache->scale_block > 16 ? cache->scale_block : 16;
     g.span_shift = log2_of(span);
-    const dim3 grid((unsigned)(T / span + 2 * n_seqs), (unsigned)(cache->n_heads + (n_q_heads + kQRows / span - 1) / (kQRows / span)));
+    const dim3 grid((unsigned)(T / span + 2 * n_seqs), (unsigned)(2 * cache->n_heads + (n_q_heads + kQRows / span - 1) / (kQRows / span)));
     if (dt == SQ_F32) return D == 64 ? launch_append<float, 64>(g, grid, st) : launch_append<float, 128>(g, grid, st);
     return D == 64 ? launch_append<__nv_bfloat16, 64>(g, grid, st) : launch_append<__nv_bfloat16, 128>(g, grid, st);
 }

@@ -58,14 +58,13 @@ struct KvAttnArgs {
 // becomes the largest s + floor(log2 vs), so that w lies inside fp16's normal range
 // for scales of any size.
 constexpr int kTile = 128;
-// Consumer warps: 12 for one side of 8 rows (152 registers each), 8 for two (224), so that
-// every accumulator stays in registers; and a warpgroup whose first two warps load.
-// 128 registers at launch times 16 warps are as many as 152 times 12 and 56 times 4;
-// 168 times 12 as many as 224 times 8 and 56 times 4.
-__host__ __device__ constexpr int consumer_warps(int NB) { return NB == 1 ? 12 : 8; }
-__host__ __device__ constexpr int attn_threads(int NB) { return 32 * (consumer_warps(NB) + 4); }
-__host__ __device__ constexpr int consumer_regs(int NB) { return NB == 1 ? 152 : 224; }
-constexpr int kProducerRegs = 56;
+// Eight consumer warps of 224 registers, so that every accumulator and a group's codes
+// stay in them (twelve of 152 spilled: 148 us for the ragged batch of 64 sequences, eight
+// 133), and a warpgroup whose first two warps load. 168 registers at launch times 12
+// warps are as many as 224 times 8 and 56 times 4.
+constexpr int kConsumers = 8;
+constexpr int kAttnThreads = 32 * (kConsumers + 4);
+constexpr int kConsumerRegs = 224, kProducerRegs = 56;
 constexpr int kGroup = 32;                    // tokens of a warp's step
 constexpr int kGroups = kTile / kGroup;
 constexpr float kMaxWeight = 256.0f;
@@ -75,14 +74,14 @@ constexpr float kNoScale = -80.0f;            // exponent that stands for scales
 // NB sides of 8 rows a warp, MT row tiles. MT == 1: the queries of a piece travel with its first tile.
 template <typename T, int D, int NB, int MT>
 struct AttnSmem {
-    static constexpr int STAGES = D == 128 ? 4 : 6;
+    static constexpr int STAGES = D == 128 ? 4 : 8;
     static constexpr int CODES = kTile * D;                              // bytes of K, and of V
     static constexpr int Q = 2 * CODES + 2 * kTile * 4;                  // behind the codes and their scales
     static constexpr int STAGE = Q + (MT == 1 ? 8 * NB * D * (int)sizeof(T) : 0);
     static constexpr int DB = D / 8;
     static constexpr int ROW = D == 128 ? 164 : 100;                     // floats of a merge row: a gap of 4 behind every DB, and
                                                                          // 4 mod 8, so that the 16-byte accesses meet no conflict
-    static constexpr int MERGE = consumer_warps(NB) * 8 * ROW * 4;
+    static constexpr int MERGE = kConsumers * 8 * ROW * 4;
     static constexpr int TOTAL = 1024 + STAGES * STAGE + MERGE;
     static_assert(STAGE % 1024 == 0, "a stage keeps the swizzle's alignment");
     static_assert(TOTAL <= 227 * 1024 - 4096, "");
@@ -176,8 +175,7 @@ struct TileWalk {
     }
 };
 
-template <int THREADS>
-__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(THREADS) : "memory"); }
+__device__ __forceinline__ void consumers_sync() { asm volatile("bar.sync 1, %0;" :: "n"(32 * kConsumers) : "memory"); }
 // An 8 x 8 matrix of 16-bit values, two of a row in each lane, transposed.
 __device__ __forceinline__ uint32_t transpose_8x8(uint32_t x) {
     uint32_t r;
@@ -199,12 +197,11 @@ __device__ __forceinline__ void attn_result(const KvAttnArgs& g, int b, int h, i
 }
 
 template <typename T, int D, int NB, int MT>
-__global__ void __launch_bounds__(attn_threads(NB), 1)
+__global__ void __launch_bounds__(kAttnThreads, 1)
 kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v, const KvAttnArgs g) {
     using S = AttnSmem<T, D, NB, MT>;
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int KS = D / 16, IT = D / 16, DB = D / 8;   // k steps of S, channel tiles of O, codes a lane holds of a value row
-    constexpr int kConsumers = consumer_warps(NB), kAttnThreads = attn_threads(NB);
     constexpr int TG = kConsumers / MT;                   // warps of a row tile
     extern __shared__ uint8_t smem_raw[];
     __shared__ __align__(8) uint64_t bars[2 * S::STAGES];
@@ -439,7 +436,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
     }
 
     // -------------------------------------------------------------------- consumers
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(consumer_regs(NB)));
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" :: "n"(kConsumerRegs));
     const int gr = lane >> 2, t4 = lane & 3;
     const int mt = warp % MT;
     int next_group = warp / MT;   // groups are dealt to the warps of a row tile in turn
@@ -704,7 +701,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                     if (spoilt) x = __int_as_float(0x7fc00000);
                     if (gr == 0) all[warp][n * 8 + 2 * t4 + e] = make_float2(m[n][e], x);
                 }
-            consumers_sync<32 * kConsumers>();
+            consumers_sync();
             const bool whole = ends && !began_before;
             const int64_t slot = (2 * (int64_t)blockIdx.x + (began_before ? 0 : 1)) * (8 * NB * MT);
 #pragma unroll
@@ -723,7 +720,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                         *reinterpret_cast<float4*>(dst + 2 * k) = make_float4(o[k][n][e] * f, o[k][n][2 + e] * f,
                                                                               o[k + 1][n][e] * f, o[k + 1][n][2 + e] * f);
                 }
-                consumers_sync<32 * kConsumers>();
+                consumers_sync();
                 for (int u = tid; u < MT * 8 * (D / 4); u += 32 * kConsumers) {
                     const int d = u % (D / 4) * 4, rr = u / (D / 4) % 8, rm = u / (2 * D);
                     const int row = (rm * NB + n) * 8 + rr;
@@ -746,7 +743,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                         *reinterpret_cast<float4*>(g.part_o + (slot + row) * D + d) = acc;
                     }
                 }
-                if (n + 1 < NB) consumers_sync<32 * kConsumers>();
+                if (n + 1 < NB) consumers_sync();
             }
             ++piece;
         }
@@ -866,7 +863,7 @@ sq_status launch_kv_attention(const CUtensorMap& mk, const CUtensorMap& mv, cons
     constexpr size_t smem = AttnSmem<T, D, NB, MT>::TOTAL;
     sq_status r = ensure_smem_attr(kv_attention_kernel<T, D, NB, MT>, smem, attr_done[di.device & 63]);
     if (r != SQ_OK) return r;
-    r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, NB, MT>, dim3(di.sm_count), dim3(attn_threads(NB)), smem, st, 1,
+    r = launch_pdl("kv_attention_kernel", kv_attention_kernel<T, D, NB, MT>, dim3(di.sm_count), dim3(kAttnThreads), smem, st, 1,
                    mk, mv, g);
     if (r != SQ_OK) return r;
     const int rows = g.n_q_heads / g.c.n_heads * g.q_len;
