@@ -549,7 +549,7 @@ sq_status sq_kv_read(const sq_kv_cache* cache, const int32_t* block_table, int64
  *   out [n_seqs x q_len x n_q_heads x head_dim], dtype dt, contiguous.
  *   lse [n_seqs x q_len x n_q_heads] float or NULL.
  *   seq_len [n_seqs] int32, device: tokens in the cache, the new ones among them.
- *   n_q_heads a multiple of n_heads; q_len * g <= 128; finite q; scale finite.
+ *   n_q_heads a multiple of n_heads; q_len * g <= 128; finite q; |scale| <= 1e38.
  *   bf16 q is exact in the products (fp16 after a power-of-two scale, what
  *   rounds is below 2^-24 of the row's largest value), fp32 q is split in two
  *   fp16 parts; sums, maxima and accumulators are fp32; the probabilities are
@@ -574,7 +574,7 @@ sq_status sq_kv_attention(const void* q, int64_t q_stride, sq_dtype dt, const sq
  *   heads contiguous, tokens q_stride, k_stride, v_stride elements apart
  *   (multiples of 8). out [T x n_q_heads x head_dim] bf16 contiguous;
  *   lse [T x n_q_heads] float or NULL: log sum exp of the row's scaled scores.
- *   head_dim 64 or 128. Scores and sums in fp32; probabilities are rounded to
+ *   head_dim 64 or 128; |scale| <= 1e38. Scores and sums in fp32; probabilities are rounded to
  *   bf16 for the second product. A sequence's own values must be finite.
  *   Offsets outside [0, T] or descending are cut, and sq_get_status() reports SQ_ERR_BOUNDS.
  *   T <= 2^30 / n_q_heads, n_seqs <= 65536. */

@@ -312,7 +312,7 @@ def test_attention_strided_queries_and_supplied_buffers():
     pg = Pages(lens, h, d, 16, 16, seed=12)
     g = torch.Generator().manual_seed(2)
     qkv = torch.randn((3 * 2, hq + 2 * h, d), generator=g).bfloat16().to(DEV)
-    q = qkv[:, :hq].view(3, 2, hq, d) if False else qkv.view(3, 2, hq + 2 * h, d)[:, :, :hq]
+    q = qkv.view(3, 2, hq + 2 * h, d)[:, :, :hq]
     out = torch.empty((3, 2, hq, d), dtype=torch.bfloat16, device=DEV)
     lse = torch.empty((3, 2, hq), device=DEV)
     ws = torch.full((max(256, sq.sq_kv_attention_workspace_size(pg.cache, 3, 2, hq)),), 255, dtype=torch.uint8, device=DEV)

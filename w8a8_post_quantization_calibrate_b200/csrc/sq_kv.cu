@@ -77,6 +77,10 @@ sq_status check_rows(const void* p, int64_t stride, int64_t width, int es, const
     return SQ_OK;
 }
 
+// What an earlier kernel of the stream may have written is read by plain loads behind
+// pdl_wait(), never as read-only data (ld.global.nc): these kernels are launched before
+// that kernel has ended, and only plain loads are promised to see its writes.
+//
 // The last b in [0, n) with at(b) <= u, for ascending `at` with at(0) <= u: 32
 // candidates at once, so two dependent loads for up to 1024 sequences. Any
 // values give a result in [0, n). All lanes of the warp take part.
@@ -163,7 +167,7 @@ __device__ __forceinline__ void rotate_lane(float (&xa)[8], float (&xb)[8], cons
         const float4* tb = reinterpret_cast<const float4*>(cs + 8 * (c + (rot >> 4)));
 #pragma unroll
         for (int i = 0; i < 2; ++i) {
-            const float4 u = __ldg(ta + i), w = __ldg(tb + i);
+            const float4 u = ta[i], w = tb[i];
             turn(xa[4 * i], xa[4 * i + 1], u.x, u.y);
             turn(xa[4 * i + 2], xa[4 * i + 3], u.z, u.w);
             turn(xb[4 * i], xb[4 * i + 1], w.x, w.y);
@@ -173,7 +177,7 @@ __device__ __forceinline__ void rotate_lane(float (&xa)[8], float (&xb)[8], cons
         const float4* t = reinterpret_cast<const float4*>(cs + 16 * c);
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
-            const float4 u = __ldg(t + i);
+            const float4 u = t[i];
             turn(xa[2 * i], xb[2 * i], u.x, u.y);
             turn(xa[2 * i + 1], xb[2 * i + 1], u.z, u.w);
         }
@@ -226,7 +230,9 @@ __device__ __forceinline__ uint2 requantize(uint2 w, float was, float s) {
 // position, z' = z (cos w + i sin w): four fp64 products an entry in place of a sincos. Each
 // turn adds at most some 2^-52, so 32 of them stay far below the one rounding to fp32
 // (2^-24). Longer runs amortise the two sincos and the power, shorter ones fill the GPU:
-// 131,072 positions x 64 frequencies took 32 us with a sincos for every entry.
+// 131,072 positions x 64
+// frequencies (67 MB) take 13.5 us, 0.76 of the measured copy rate; with a sincos for every
+// entry they took 32.
 struct RopeFreq {
     double theta, factor, low, high, orig, magnitude;
 };
@@ -297,13 +303,13 @@ rope_append_kernel(const AppendArgs g) {
     const int64_t u = blockIdx.x;
     const int32_t* cu = g.cu;
     const int sh = g.span_shift;
-    auto start_of = [&](int b) { return (int64_t)(__ldg(cu + b) >> sh) + 2 * (int64_t)b; };
+    auto start_of = [&](int b) { return (int64_t)(*(cu + b) >> sh) + 2 * (int64_t)b; };
     if (u >= start_of(g.n_seqs)) return;
     const int b = warp_find(start_of, g.n_seqs, u);
     const int64_t j = u - start_of(b);
-    const int64_t t0 = max(0, __ldg(cu + b));
-    const int64_t n = min((int64_t)__ldg(cu + b + 1), g.T) - t0;
-    const int64_t ctx = __ldg(g.ctx_len + b);
+    const int64_t t0 = max(0, *(cu + b));
+    const int64_t n = min((int64_t)*(cu + b + 1), g.T) - t0;
+    const int64_t ctx = *(g.ctx_len + b);
     if (j < 0 || n <= 0) return;
     const int64_t span0 = ctx < 0 ? j << sh : ((ctx >> sh) + j) << sh;      // first position of the span
     const int64_t lo = max(span0, ctx), hi = min(span0 + (1 << sh), max((int64_t)0, ctx) + n);
@@ -362,7 +368,7 @@ rope_append_kernel(const AppendArgs g) {
     const int r0 = threadIdx.x / LPR;
     int64_t page = -1;
     if (lo < ok) {
-        page = __ldg(g.block_table + b * g.max_pages + (span0 >> g.c.page_shift));
+        page = *(g.block_table + b * g.max_pages + (span0 >> g.c.page_shift));
         if ((uint64_t)page >= (uint64_t)g.c.n_pages) {
             if (threadIdx.x == 0) record_status(SQ_ERR_BOUNDS, SITE_KV_APPEND);
             page = -1;
@@ -450,10 +456,13 @@ rope_append_kernel(const AppendArgs g) {
 }
 
 // ================================================================== read back
+// A lane has 16 codes of K and of V of one (token, head): 16-byte loads, whole sectors both
+// ways. Bound by HBM: 870 MB of sixteen prefixes of 32 heads in 151 us, 0.88 of the
+// measured copy rate.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)
-kv_read_kernel(const KvView g, const int32_t* __restrict__ block_table, int64_t max_pages, const int32_t* __restrict__ first,
-               const int32_t* __restrict__ cu, int n_seqs, int64_t rows, T* __restrict__ k_out, T* __restrict__ v_out) {
+kv_read_kernel(const KvView g, const int32_t* block_table, int64_t max_pages, const int32_t* first, const int32_t* cu, int n_seqs,
+               int64_t rows, T* k_out, T* v_out) {
     constexpr int LPR = D / 16;
     pdl_wait();
     pdl_trigger();
@@ -461,17 +470,17 @@ kv_read_kernel(const KvView g, const int32_t* __restrict__ block_table, int64_t 
     const int64_t flat = id / LPR;
     const int c = (int)(id % LPR);
     // the block's first row by search, the thread's own from there
-    const int64_t total = min(rows, (int64_t)__ldg(cu + n_seqs));
+    const int64_t total = min(rows, (int64_t)*(cu + n_seqs));
     const int64_t t_block = (int64_t)blockIdx.x * (256 / LPR) / g.n_heads;
     if (t_block >= total) return;
-    int b = warp_find([&](int i) { return (int64_t)__ldg(cu + i); }, n_seqs, t_block);
+    int b = warp_find([&](int i) { return (int64_t)*(cu + i); }, n_seqs, t_block);
     const int64_t t = flat / g.n_heads;
     if (t >= total) return;
-    while (b + 1 < n_seqs && __ldg(cu + b + 1) <= t) ++b;
+    while (b + 1 < n_seqs && *(cu + b + 1) <= t) ++b;
     const int h = (int)(flat % g.n_heads);
-    const int64_t p = (int64_t)__ldg(first + b) + t - __ldg(cu + b);
+    const int64_t p = (int64_t)*(first + b) + t - *(cu + b);
     int64_t page = -1;
-    if (p >= 0 && p < (max_pages << g.page_shift)) page = __ldg(block_table + b * max_pages + (p >> g.page_shift));
+    if (p >= 0 && p < (max_pages << g.page_shift)) page = *(block_table + b * max_pages + (p >> g.page_shift));
     const bool ok = (uint64_t)page < (uint64_t)g.n_pages;
     if (!ok && c == 0) record_status(SQ_ERR_BOUNDS, SITE_KV_READ);
     const int64_t ph = ok ? page * g.n_heads + h : 0;
