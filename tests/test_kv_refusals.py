@@ -123,6 +123,10 @@ def test_the_binding_checks_shapes_before_the_call(sq):
     with pytest.raises(ValueError, match="CUDA"):
         c = sq.KvCache.empty(2, 1, 64, 16, 16, device="cpu")
         sq.sq_kv_attention(torch.zeros((1, 1, 1, 64)), c, torch.zeros((1, 1), dtype=torch.int32), torch.zeros(1, dtype=torch.int32))
+    with pytest.raises(ValueError, match="CUDA"):
+        sq.sq_rope_table(4, 16, table=torch.zeros((4, 8, 2)))
+    with pytest.raises(ValueError, match="CUDA"):
+        sq.sq_rope_table(4, 16, device="cpu")
     c = sq.KvCache.empty(2, 1, 64, 16, 16, device="cpu")
     with pytest.raises(ValueError, match="same shapes"):
         sq._cache_bytes(sq.KvCache(c.k, c.v[:1], c.k_scale, c.v_scale))

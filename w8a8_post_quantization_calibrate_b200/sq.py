@@ -562,7 +562,7 @@ class KvCache(typing.NamedTuple):
 
 def _ptr(t: torch.Tensor, dtype, index: int, name: str) -> int:
     """The address of a contiguous tensor of `dtype` on CUDA device `index`."""
-    if t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
+    if index < 0 or t.get_device() != index or t.dtype is not dtype or not t.is_contiguous():
         if not t.is_cuda:
             raise ValueError(f"{name} must be a CUDA tensor")
         if t.dtype is not dtype:
