@@ -801,19 +801,22 @@ __global__ void __launch_bounds__(128) kv_attention_join_kernel(const KvAttnArgs
         for (int e = 0; e < E; ++e) acc[e] *= old;
         const unsigned have = __ballot_sync(0xffffffffu, some);
         const int n = 32 - __clz(inside);
-#pragma unroll 4
-        for (int p = 0; p < n; ++p) {
+#pragma unroll 8
+        for (int p = 0; p < n; ++p) {   // no branch, so that several pieces' loads are in flight
             const float fp = __shfl_sync(0xffffffffu, f, p);
-            if (!((have >> p) & 1u)) continue;
+            const bool is = (have >> p) & 1u;   // an empty share's slot holds anything
             const int cp = i - 1 + p0 + p;
             const float* o = g.part_o + ((2 * (int64_t)cp + (cp == i - 1 ? 1 : 0)) * slot_rows + row) * D + lane * E;
+            float v[E];
             if constexpr (E == 4) {
-                const float4 v = *reinterpret_cast<const float4*>(o);
-                acc[0] += v.x * fp; acc[1] += v.y * fp; acc[2] += v.z * fp; acc[3] += v.w * fp;
+                const float4 x = *reinterpret_cast<const float4*>(o);
+                v[0] = x.x; v[1] = x.y; v[2] = x.z; v[3] = x.w;
             } else {
-                const float2 v = *reinterpret_cast<const float2*>(o);
-                acc[0] += v.x * fp; acc[1] += v.y * fp;
+                const float2 x = *reinterpret_cast<const float2*>(o);
+                v[0] = x.x; v[1] = x.y;
             }
+#pragma unroll
+            for (int e = 0; e < E; ++e) acc[e] += is ? v[e] * fp : 0.0f;
         }
         if (inside != 0xffffffffu) break;
     }
