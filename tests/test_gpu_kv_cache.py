@@ -386,3 +386,35 @@ def test_offsets_beyond_32_bits():
     want = torch.einsum("ht,thd->hd", w, v.double())
     assert (out[0, 0].double() - want).abs().max() <= 1e-4 * v.abs().max()
     assert sq.sq_get_status() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("d,dtype,rows,tiles", [(128, torch.bfloat16, 1, 4), (128, torch.float32, 16, 4), (64, torch.bfloat16, 16, 8),
+                                                (64, torch.float32, 1, 8), (128, torch.bfloat16, 8, 1), (128, torch.bfloat16, 2, 5)])
+def test_attention_of_sequences_as_long_as_the_ring(d, dtype, rows, tiles):
+    """Every fourth tile of 128 tokens (eighth for heads of 64) takes the place of an earlier one
+    in shared memory; here it brings another sequence's queries there, and for every third
+    sequence a bad page."""
+    seqs, n, ps = 500, 128 * tiles, 64
+    pg = Pages([n] * 2, 1, d, ps, 16, seed=tiles + d)
+    table = pg.dev_table[torch.arange(seqs, device=DEV) % 2].contiguous()
+    table[2::3, n // ps - 1] = pg.n
+    g = torch.Generator().manual_seed(rows)
+    q = torch.randn((seqs, 1, rows, d), generator=g).to(dtype).to(DEV)
+    lens = ints([n] * seqs)
+    out, lse = sq.sq_kv_attention(q, pg.cache, table, lens, want_lse=True)
+    assert sq.sq_get_status() == sq.SQ_ERR_BOUNDS and sq.sq_get_status() == sq.SQ_OK
+    bad = torch.arange(seqs, device=DEV) % 3 == 2
+    assert torch.isnan(out[bad]).all() and torch.isnan(lse[bad]).all()
+    for i in range(10):
+        again = sq.sq_kv_attention(q, pg.cache, table, lens)
+        assert torch.equal(again[~bad], out[~bad]), "two calls differ"
+    for p in range(2):   # sequences on the same pages as rows of one product
+        mine = torch.nonzero(~bad & (torch.arange(seqs, device=DEV) % 2 == p)).flatten()
+        k, v = (ref.held(c, s, pg.table[p], 0, n)[:, 0] for c, s in ((pg.k, pg.ks), (pg.v, pg.vs)))
+        qn = q[mine].float().cpu().numpy().reshape(-1, d)
+        f32 = dtype == torch.float32
+        want, wlse, bound, lbound = ref.attention(qn, k, v, d ** -0.5, np.ones((len(qn), n), bool), 2.0 ** -22 if f32 else 2.0 ** -11,
+                                                  2.0 ** -24 if f32 else 2.0 ** -8, q_step=2.0 ** -24)
+        assert np.all(np.abs(out[mine].float().cpu().numpy().reshape(-1, d) - want) <= bound)
+        assert np.all(np.abs(lse[mine].cpu().numpy().reshape(-1) - wlse) <= lbound)
+    assert sq.sq_get_status() == sq.SQ_ERR_BOUNDS

@@ -529,6 +529,10 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                     see[n][e] = r < R ? max(0, see_all + r / G) : 0;
                 }
             }
+            // With one row tile half of the warps have no group in this tile and so no say in
+            // when its stage is free, but they have read the queries and the flag there:
+            // nobody frees it before all have. (With more, every warp has a group.)
+            if (MT == 1) consumers_sync();
         }
 #pragma unroll 1
         for (; next_group < kGroups; next_group += TG) {
