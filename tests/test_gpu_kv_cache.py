@@ -418,3 +418,82 @@ def test_attention_of_sequences_as_long_as_the_ring(d, dtype, rows, tiles):
         assert np.all(np.abs(out[mine].float().cpu().numpy().reshape(-1, d) - want) <= bound)
         assert np.all(np.abs(lse[mine].cpu().numpy().reshape(-1) - wlse) <= lbound)
     assert sq.sq_get_status() == sq.SQ_ERR_BOUNDS
+
+
+def _value_scales(mode, vs, lens, table, ps, sb):
+    """Value scales [pages, heads, blocks] of a test of zero and very unlike scales."""
+    for b, n in enumerate(lens):
+        for s0 in range(0, n, sb):
+            at = (table[b, s0 // ps], slice(None), s0 % ps // sb)
+            if mode == "all zero":
+                vs[at] = 0.0
+            elif mode == "first 32 zero":
+                vs[at] *= s0 >= 32
+            elif mode == "every other 32 zero":
+                vs[at] *= s0 // 32 % 2
+            elif mode == "first 640 zero":
+                vs[at] *= s0 >= 640
+            elif mode == "zero, tiny and ordinary":
+                vs[at] *= (0.0, 2.0 ** -60, 1.0)[s0 // 16 % 3]
+            elif mode == "2^-70 to 2^90":
+                vs[at] *= 2.0 ** ((s0 // 16 * 37) % 161 - 70)
+            elif mode == "near 1e30":
+                vs[at] *= 2.0 ** 100
+
+
+MODES = ["all zero", "first 32 zero", "every other 32 zero", "first 640 zero", "zero, tiny and ordinary", "2^-70 to 2^90", "near 1e30"]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("mode", MODES)
+def test_attention_of_zero_and_very_unlike_value_scales(mode, dtype):
+    """Blocks of zero values (scale 0, as the append writes them) anywhere, a lone token among them;
+    sequences of one CTA and sequences that many share; codes that a scale of 0 makes 0."""
+    lens, hq, h, d, ps, sb = [1, 20, 32, 33, 700, 5000], 6, 2, 128, 64, 16
+    pg = Pages(lens, h, d, ps, sb, seed=21)
+    _value_scales(mode, pg.vs, lens, pg.table, ps, sb)
+    pg.cache.v_scale.copy_(torch.from_numpy(pg.vs))
+    for l in (1, 5, 40):
+        g = torch.Generator().manual_seed(l)
+        q = torch.randn((len(lens), l, hq, d), generator=g).to(dtype).to(DEV)
+        out, lse = sq.sq_kv_attention(q, pg.cache, pg.dev_table, ints(lens), want_lse=True)
+        assert sq.sq_get_status() == sq.SQ_OK
+        check_attention(pg, lens, q, out, lse, d ** -0.5, dtype, what=f"{mode}, {l} tokens,")
+        if mode == "all zero":
+            assert not out.any() and not torch.isnan(lse).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("steps", [40, 90, 200, 2000])
+def test_attention_of_a_zero_value_with_a_score_far_above(steps, dtype):
+    """Tokens of zero value whose scores are `steps` powers of two above all others, behind groups of
+    ordinary ones in the same warp's share: the sum of the weights stays finite."""
+    n, seqs, d, ps, sb = 1536, 300, 64, 64, 16
+    pg = Pages([n], 1, d, ps, sb, seed=22)
+    pg.k[:] = 0
+    pg.ks[:] = 0.02
+    high = np.arange(n) // sb % 40 == 30
+    for p in np.nonzero(high)[0]:
+        pg.k[pg.table[0, p // ps], 0, p % ps, 0] = 100
+        pg.vs[pg.table[0, p // ps], 0, p % ps // sb] = 0.0
+    for mine, theirs in zip((pg.k, pg.ks, pg.vs), (pg.cache.k, pg.cache.k_scale, pg.cache.v_scale)):
+        theirs.copy_(torch.from_numpy(mine))
+    q = torch.zeros((seqs, 1, 2, d), device=DEV)
+    q[:, :, 0, 0] = 1.0      # head 1 is flat
+    scale = steps * np.log(2.0) / (100 * 0.02)
+    out, lse = sq.sq_kv_attention(q.to(dtype), pg.cache, pg.dev_table.expand(seqs, -1).contiguous(), ints([n] * seqs), scale=scale, want_lse=True)
+    assert sq.sq_get_status() == sq.SQ_OK
+    # the others have a score of 0 beside `high` of them at `steps` octaves
+    v = ref.held(pg.v, pg.vs, pg.table[0], 0, n)[:, 0].astype(np.float64)
+    for head, w in ((0, 2.0 ** -float(min(steps, 1000))), (1, 1.0)):
+        p = np.where(high, 1.0, w)
+        want = p @ v / p.sum()
+        # fp16 weights (two parts for fp32) and their floor of 2^-25 of the reference's weight, sums over n, the output's rounding
+        step, last = (2.0 ** -22, 2.0 ** -24) if dtype == torch.float32 else (2.0 ** -11, 2.0 ** -8)
+        a = p @ np.abs(v) / p.sum()
+        e = 2.0 ** -21 * (steps + 8) + 64 * 2.0 ** -23 * steps
+        bound = 1.1 * ((step + 2 * e + n * 2.0 ** -23) * a + n * 2.0 ** -25 * w * np.abs(v).max() / p.sum() + last * np.abs(want)) + 1e-38
+        got = out[:, 0, head].float().cpu().numpy()
+        assert np.all(np.abs(got - want) <= bound), (head, np.max(np.abs(got - want) / bound))
+        true = np.log(p.sum()) + (0.0 if head else steps * np.log(2.0))
+        assert np.all(np.abs(lse[:, 0, head].cpu().numpy() - true) <= 1.1 * (e + n * 2.0 ** -23) + 2.0 ** -20 * abs(true) + 2.0 ** -22)

@@ -56,9 +56,9 @@ struct KvAttnArgs {
 //   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
 //   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
 // w = 2^(s - m) vs goes to the second product, 2^(s - m) into the sum. The reference m is
-// moved only when some |w| is above 2^8 (rare after the first groups); then it
-// becomes the largest s + floor(log2 vs), so that w lies inside fp16's normal range
-// for scales of any size.
+// moved only when some |w|, or a lane's sum times 2^-80, is above 2^8 (rare after the first
+// groups); then it becomes the largest s + max(floor(log2 vs), -80), so that the largest w
+// lies in fp16's normal range for scales from 2^-80 up.
 constexpr int kTile = 128;
 // Eight consumer warps of 224 registers, so that every accumulator and a group's codes
 // stay in them (twelve of 152 spilled: 148 us for the ragged batch of 64 sequences, eight
@@ -71,7 +71,10 @@ constexpr int kGroup = 32;                    // tokens of a warp's step
 constexpr int kGroups = kTile / kGroup;
 constexpr float kMaxWeight = 256.0f;
 constexpr float kNoReference = -1.0e30f;      // nothing seen yet: 2^(s - m) is infinite for any score, 0 for a masked one
-constexpr float kNoScale = -80.0f;            // exponent that stands for scales below 2^-80: 2^88 times 2^30 tokens is finite
+// Scales below 2^-80, zero among them, count as 2^-80 where the reference is chosen and where it
+// is found too low: a weight of 2^(s - m) that its value's scale makes small or zero could
+// overflow in the sum otherwise. A lane's sum over a group stays below 2^88, that of 2^30 tokens is finite.
+constexpr float kNoScale = -80.0f, kLeastScale = 0x1p-80f;
 
 // NB sides of 8 rows a warp, MT row tiles. MT == 1: the queries of a piece travel with its first tile.
 template <typename T, int D, int NB, int MT>
@@ -626,6 +629,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                             wt[j >> 1][n][2 * (j & 1) + e] = a * vs[j];
                             most = fmaxf(most, fabsf(a * vs[j]));
                         }
+                    most = fmaxf(most, fmaxf(sum[n][0], sum[n][1]) * kLeastScale);
                 }
             };
             float most;
