@@ -553,7 +553,9 @@ sq_status sq_kv_read(const sq_kv_cache* cache, const int32_t* block_table, int64
  *   bf16 q is exact in the products (fp16 after a power-of-two scale, what
  *   rounds is below 2^-24 of the row's largest value), fp32 q is split in two
  *   fp16 parts; sums, maxima and accumulators are fp32; the probabilities are
- *   rounded to fp16 (two fp16 parts for fp32 q).
+ *   rounded to fp16 (two fp16 parts for fp32 q) and keep at least 2^-32 of the row's
+ *   largest (probability * value scale), where scales below 2^-80 count as 2^-80. Value
+ *   scales up to 2^100.
  *   workspace: device, 256-byte aligned, ws_bytes >= sq_kv_attention_workspace_size(...)
  *     on the same device; it needs no initialisation and holds nothing between
  *     calls. Calls that share one must not overlap on the GPU. */

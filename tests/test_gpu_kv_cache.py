@@ -497,3 +497,34 @@ def test_attention_of_a_zero_value_with_a_score_far_above(steps, dtype):
         assert np.all(np.abs(got - want) <= bound), (head, np.max(np.abs(got - want) / bound))
         true = np.log(p.sum()) + (0.0 if head else steps * np.log(2.0))
         assert np.all(np.abs(lse[:, 0, head].cpu().numpy() - true) <= 1.1 * (e + n * 2.0 ** -23) + 2.0 ** -20 * abs(true) + 2.0 ** -22)
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("steps", [12.3, 20.02, 25.02, 28.5])
+def test_attention_of_many_small_weights_beside_a_large_one(steps, dtype):
+    """One token of zero value weighs 2^steps times as much as each of 32,767 others, which are all of the
+    result: a weight keeps 2^-32 of the largest, or fp16's relative 2^-11 (fp32: 2^-22)."""
+    n, d, ps, sb = 32768, 64, 128, 128
+    seqs = torch.cuda.get_device_properties(0).multi_processor_count   # a whole sequence for each CTA
+    pg = Pages([n], 1, d, ps, sb, seed=23)
+    pg.k[:] = 0
+    pg.k[pg.table[0, 0], 0, 0, 0] = 100
+    pg.v = np.abs(pg.v.astype(np.int16)).clip(60, 127).astype(np.int8)
+    pg.v[pg.table[0, 0], 0, 0] = 0
+    pg.ks[:], pg.vs[:] = 2.0 ** -6, 2.0 ** -5
+    for mine, theirs in zip((pg.k, pg.v, pg.ks, pg.vs), pg.cache):
+        theirs.copy_(torch.from_numpy(mine))
+    q = torch.zeros((seqs, 1, 1, d), device=DEV, dtype=dtype)
+    q[..., 0] = 1.0
+    scale = float(np.float32(steps * np.log(2.0) / (100 * 2.0 ** -6)))
+    out = sq.sq_kv_attention(q, pg.cache, pg.dev_table.expand(seqs, -1).contiguous(), ints([n] * seqs), scale=scale)
+    assert sq.sq_get_status() == sq.SQ_OK
+    v = ref.held(pg.v, pg.vs, pg.table[0], 0, n)[:, 0].astype(np.float64)
+    p = np.full(n, np.exp(-scale * 100 * 2.0 ** -6))
+    p[0] = 1.0
+    want = p @ v / p.sum()
+    step, last = (2.0 ** -22, 2.0 ** -24) if dtype == torch.float32 else (2.0 ** -11, 2.0 ** -8)
+    e = 2.0 ** -21 * (steps + 16)      # the exponent's argument: scale, reference and difference in fp32
+    bound = 1.1 * ((step + 2 * e + n * 2.0 ** -23) * want + n * 2.0 ** -32 * v.max() / p.sum() + last * want)
+    err = np.abs(out[:, 0, 0].float().cpu().numpy() - want)
+    assert np.all(err <= bound), np.max(err / bound)

@@ -56,9 +56,11 @@ struct KvAttnArgs {
 //   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
 //   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
 // w = 2^(s - m) vs goes to the second product, 2^(s - m) into the sum. The reference m is
-// moved only when some |w|, or a lane's sum times 2^-80, is above 2^8 (rare after the first
-// groups); then it becomes the largest s + max(floor(log2 vs), -80), so that the largest w
-// lies in fp16's normal range for scales from 2^-80 up.
+// moved only when some |w|, or a lane's sum times 2^-80, is above 2^15 (rare after the first
+// groups); then it becomes the largest s + max(floor(log2 vs), -80), less 7, so that the
+// largest w is 2^7 .. 2^8 for scales from 2^-80 up: 2^8 below the limit, and 2^-32 of it is
+// what fp16's smallest step, 2^-24, leaves of small weights. (Kept at 1 .. 2, weights below 2^-25 of
+// the largest were lost: a sixth of a result that 32,767 of them made.)
 constexpr int kTile = 128;
 // Eight consumer warps of 224 registers, so that every accumulator and a group's codes
 // stay in them (twelve of 152 spilled: 148 us for the ragged batch of 64 sequences, eight
@@ -69,11 +71,13 @@ constexpr int kAttnThreads = 32 * (kConsumers + 4);
 constexpr int kConsumerRegs = 224, kProducerRegs = 56;
 constexpr int kGroup = 32;                    // tokens of a warp's step
 constexpr int kGroups = kTile / kGroup;
-constexpr float kMaxWeight = 256.0f;
+constexpr float kMaxWeight = 32768.0f;        // fp16 ends at 65504
+constexpr int kHeadroom = 7;                  // a new reference makes the largest weight 2^7 .. 2^8
 constexpr float kNoReference = -1.0e30f;      // nothing seen yet: 2^(s - m) is infinite for any score, 0 for a masked one
 // Scales below 2^-80, zero among them, count as 2^-80 where the reference is chosen and where it
 // is found too low: a weight of 2^(s - m) that its value's scale makes small or zero could
-// overflow in the sum otherwise. A lane's sum over a group stays below 2^88, that of 2^30 tokens is finite.
+// overflow in the sum otherwise. A lane's sum over its 4 tokens of a group stays below 2^95, that of
+// 2^30 tokens below 2^123.
 constexpr float kNoScale = -80.0f, kLeastScale = 0x1p-80f;
 
 // NB sides of 8 rows a warp, MT row tiles. MT == 1: the queries of a piece travel with its first tile.
@@ -638,7 +642,7 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                 float ex[4];
 #pragma unroll
                 for (int j = 0; j < 4; ++j)
-                    ex[j] = fmaxf((float)((int)((__float_as_uint(vs[j]) >> 23) & 255u) - 127), kNoScale);
+                    ex[j] = fmaxf((float)((int)((__float_as_uint(vs[j]) >> 23) & 255u) - 127 - kHeadroom), kNoScale - kHeadroom);
 #pragma unroll
                 for (int n = 0; n < NB; ++n)
 #pragma unroll
