@@ -191,3 +191,121 @@ def test_largest_row_counts_and_many_sequences():
     assert (out[:, 0] - want).abs().max() <= 2.0 ** -20 * want.abs().max()
     assert torch.isneginf(lse[lens == 0]).all() and torch.isfinite(lse[lens == 1]).all()
     assert sq.sq_get_status() == sq.SQ_OK
+
+
+def _soon_overwritten(nbytes):
+    """Leave the allocator a block of nbytes that the current stream is still to write."""
+    x = torch.empty(nbytes, dtype=torch.uint8, device=DEV)
+    torch.cuda._sleep(100_000_000)
+    x.fill_(0x7b)
+
+
+def test_results_for_a_named_stream_are_not_on_the_current_streams_memory():
+    """The caller's stream has work before it that writes memory freed since; a call on another stream,
+    which does not wait for that work, must not get this memory for its result or workspace."""
+    torch.cuda.empty_cache()
+    side = torch.cuda.Stream()
+    want = sq.sq_rope_table(4096, 128)
+    torch.cuda.synchronize()
+    _soon_overwritten(want.numel() * 4)
+    for stream in (side, side.cuda_stream):
+        got = sq.sq_rope_table(4096, 128, stream=stream)
+        torch.cuda.synchronize()
+        assert torch.equal(got, want)
+
+    h, d, n = 8, 128, 2048
+    cache = sq.KvCache.empty(n // 64, h, d)
+    g = torch.Generator().manual_seed(5)
+    x = torch.randn((n, 2 * h, d), generator=g).bfloat16().to(DEV)
+    pages, zero, cu, lens = torch.arange(n // 64, dtype=torch.int32, device=DEV).view(1, -1), ints([0]), ints([0, n]), ints([n])
+    sq.sq_rope_kv_append(None, x[:, :h], x[:, h:], cache, pages, zero, cu)
+    want = sq.sq_kv_read(cache, pages, zero, cu, n)
+    torch.cuda.synchronize()
+    for _ in range(2):
+        _soon_overwritten(n * h * d * 2)
+    got = sq.sq_kv_read(cache, pages, zero, cu, n, stream=side)
+    torch.cuda.synchronize()
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1])
+    assert sq.sq_get_status() == sq.SQ_OK
+
+
+def test_a_result_for_a_named_stream_is_kept_while_the_caller_reads_it():
+    """Freed by the caller with a read of it still to run on the current stream: its memory is not
+    given to the named stream's next result before that."""
+    side = torch.cuda.Stream()
+    torch.cuda.synchronize()
+    want = sq.sq_rope_table(4096, 128)
+    for _ in range(3):
+        t = sq.sq_rope_table(4096, 128, stream=side)
+        torch.cuda.current_stream().wait_stream(side)
+        torch.cuda._sleep(50_000_000)
+        copy = t.clone()
+        del t
+        other = sq.sq_rope_table(4096, 128, first_pos=77, stream=side)
+        torch.cuda.synchronize()
+        assert torch.equal(copy, want)
+        del other
+    assert sq.sq_get_status() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("handle", [False, True])
+def test_all_calls_on_a_named_stream(handle):
+    """The same results as on the current stream, whose memory is about to be overwritten; the
+    default stream named while another is the current one."""
+    lens, hq, h, d = [70, 33], 6, 2, 64
+    t = sum(lens)
+    g = torch.Generator().manual_seed(7)
+    x = torch.randn((t, hq + 2 * h, d), generator=g).bfloat16().to(DEV)
+    pages, zero, cu, n = ints(range(10)).view(2, 5), ints([0, 0]), ints([0, 70, 103]), ints(lens)
+
+    def calls(stream):
+        cache = sq.KvCache(*(c.clone() for c in blank))
+        torch.cuda.synchronize()
+        if stream is not None:
+            for size in (96 * 32 * 8, t * hq * d * 2, t * h * d * 2, 4_000_000):
+                _soon_overwritten(size)
+        table = sq.sq_rope_table(96, d, stream=stream)
+        q, k = sq.sq_rope_kv_append(x[:, :hq], x[:, hq:hq + h], x[:, hq + h:], cache, pages, zero, cu, table=table, want_k=True, stream=stream)
+        kr, vr = sq.sq_kv_read(cache, pages, zero, cu, t, stream=stream)
+        a, al = sq.sq_kv_attention(q[[69, 102]].view(2, 1, hq, d) if stream is None else last, cache, pages, n, want_lse=True, stream=stream)
+        p, pl = sq.sq_prompt_attention(q, k, x[:, hq + h:], cu, want_lse=True, stream=stream)
+        torch.cuda.synchronize()
+        return table, q, k, kr, vr, a, al, p, pl, *cache
+
+    side = torch.cuda.Stream()
+    blank = sq.KvCache.empty(10, h, d, page_size=16, scale_block=4)
+    for c in blank:
+        c.zero_()
+    want = calls(None)
+    last = want[1][[69, 102]].view(2, 1, hq, d)
+    torch.cuda.synchronize()
+    assert all(torch.equal(a, b) for a, b in zip(calls(side.cuda_stream if handle else side), want))
+    assert all(torch.equal(a, b) for a, b in zip(calls(torch.cuda.current_stream()), want))
+    with torch.cuda.stream(side):
+        got = calls(0 if handle else torch.cuda.default_stream())
+    assert all(torch.equal(a, b) for a, b in zip(got, want))
+    assert sq.sq_get_status() == sq.SQ_OK
+
+
+def test_a_named_stream_inside_a_capture():
+    cache = sq.KvCache(*(c.zero_() for c in sq.KvCache.empty(4, 1, 64, page_size=16, scale_block=16)))
+    cache.k_scale.fill_(0.01)
+    cache.v.fill_(5)
+    cache.v_scale.fill_(0.5)
+    pages, n = ints(range(4)).view(1, 4), ints([60])
+    q = torch.randn((1, 1, 4, 64), device=DEV)
+    sq.sq_kv_attention(q, cache, pages, n)
+    torch.cuda.synchronize()
+    graph, side = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    with torch.cuda.graph(graph):
+        main = torch.cuda.current_stream()
+        side.wait_stream(main)
+        a = sq.sq_kv_attention(q, cache, pages, n, stream=side)
+        b = sq.sq_kv_attention(q, cache, pages, n)
+        main.wait_stream(side)
+    for _ in range(3):
+        a.zero_(), b.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(a, b) and (a - 2.5).abs().max() <= 2.5 * 2.0 ** -20
+    assert sq.sq_get_status() == sq.SQ_OK

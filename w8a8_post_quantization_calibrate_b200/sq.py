@@ -614,19 +614,29 @@ def _token_rows(t: torch.Tensor, index: int, name: str) -> tuple[int, int]:
     return t.data_ptr(), step
 
 
-def _made(like: torch.Tensor, shape, dtype, stream) -> torch.Tensor:
-    """A tensor on like's device that the call on `stream` writes; known to the
-    allocator as in use there when that is not the current stream."""
-    t = like.new_empty(shape, dtype=dtype)
-    if stream is not None:
-        t.record_stream(stream if isinstance(stream, torch.cuda.Stream) else torch.cuda.ExternalStream(int(stream), t.device))
+def _made(device: torch.device, shape, dtype, stream) -> torch.Tensor:
+    """A new tensor that the call on `stream` writes. On another stream than the
+    current one its memory is that stream's, which does not wait for what the
+    current stream still does with memory freed there; the current stream is
+    noted as a reader."""
+    if stream is None:
+        return torch.empty(shape, dtype=dtype, device=device)
+    current = torch.cuda.current_stream(device)
+    if not isinstance(stream, torch.cuda.Stream):
+        raw = int(stream)
+        stream = torch.cuda.ExternalStream(raw, device) if raw else torch.cuda.default_stream(device)
+    if stream.cuda_stream == current.cuda_stream:
+        return torch.empty(shape, dtype=dtype, device=device)
+    with torch.cuda.stream(stream):
+        t = torch.empty(shape, dtype=dtype, device=device)
+    t.record_stream(current)
     return t
 
 
 def _given_or_made(t, like: torch.Tensor, shape, dtype, index: int, stream, name: str):
     """-> (t, its address); a new tensor if t is None."""
     if t is None:
-        t = _made(like, shape, dtype, stream)
+        t = like.new_empty(shape, dtype=dtype) if stream is None else _made(like.device, shape, dtype, stream)
         return t, t.data_ptr()
     return t, _shaped(t, shape, dtype, index, name)
 
@@ -659,10 +669,7 @@ def sq_rope_table(n_pos: int, rot_dim: int, theta: float = 10000.0, first_pos: i
         device = torch.device("cuda" if device is None else device)
         if device.type != "cuda":
             raise ValueError("the table is a CUDA tensor")
-        table = torch.empty(shape, dtype=torch.float32, device=device)
-        if stream is not None:
-            table.record_stream(stream if isinstance(stream, torch.cuda.Stream) else
-                                torch.cuda.ExternalStream(int(stream), table.device))
+        table = _made(device, shape, torch.float32, stream)
     index = table.get_device()
     ptr = _shaped(table, shape, torch.float32, index, "table")
     scaling = _ROPE_SCALING.pack(factor, low_turns, high_turns, original_len, magnitude)
@@ -758,8 +765,7 @@ def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, 
     if workspace is None:
         # the size goes by the device's SMs, which are alike on every device of a node
         ws_bytes = _lib.sq_kv_attention_workspace_size(c, n_seqs, q_len, hq)
-        workspace = _made(q, (ws_bytes,), torch.uint8, stream)
-        ws = workspace.data_ptr()
+        workspace, ws = _given_or_made(None, q, (ws_bytes,), torch.uint8, index, stream, "workspace")
     else:
         ws_bytes = workspace.numel()
         ws = _ptr(workspace, torch.uint8, index, "workspace")
