@@ -530,8 +530,8 @@ sq_status sq_rope_kv_append(const sq_kv_cache* cache, const int32_t* block_table
 /* sq_kv_read: cached tokens as values. Row r of the outputs is position
  *   first[b] + r - cu_out[b] of the sequence b with cu_out[b] <= r < cu_out[b+1],
  *     out = RN(code * scale), rounded once more for SQ_BF16.
- *   first [n_seqs], cu_out [n_seqs + 1] int32, device; T rows in the outputs; rows from
- *   cu_out[n_seqs] on are left as they were.
+ *   first [n_seqs], cu_out [n_seqs + 1] int32, ascending, device; T rows in the outputs; rows
+ *   in front of cu_out[0] and from cu_out[n_seqs] on are left as they were.
  *   k_out, v_out [T x n_heads x head_dim], dtype dt (SQ_F32 or SQ_BF16), contiguous. */
 sq_status sq_kv_read(const sq_kv_cache* cache, const int32_t* block_table, int64_t max_pages, const int32_t* first,
                      const int32_t* cu_out, int64_t n_seqs, int64_t T, void* k_out, void* v_out, sq_dtype dt,

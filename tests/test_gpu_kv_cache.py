@@ -528,3 +528,15 @@ def test_attention_of_many_small_weights_beside_a_large_one(steps, dtype):
     bound = 1.1 * ((step + 2 * e + n * 2.0 ** -23) * want + n * 2.0 ** -32 * v.max() / p.sum() + last * want)
     err = np.abs(out[:, 0, 0].float().cpu().numpy() - want)
     assert np.all(err <= bound), np.max(err / bound)
+
+
+def test_read_leaves_rows_before_the_first_sequence():
+    """Rows that no sequence has, in front of the first and behind the last one, stay as they were."""
+    pg = Pages([50, 20], 3, 64, 16, 4, seed=31)
+    k, v = (torch.full((60, 3, 64), 5.0, device=DEV) for _ in range(2))
+    sq.sq_kv_read(pg.cache, pg.dev_table, ints([17, 2]), ints([9, 30, 48]), 60, k_out=k, v_out=v)
+    assert sq.sq_get_status() == sq.SQ_OK
+    for got, codes, scales in ((k, pg.k, pg.ks), (v, pg.v, pg.vs)):
+        got = got.cpu().numpy()
+        want = np.concatenate([ref.held(codes, scales, pg.table[0], 17, 38), ref.held(codes, scales, pg.table[1], 2, 20)])
+        assert np.array_equal(got[9:48], want) and np.all(got[:9] == 5.0) and np.all(got[48:] == 5.0)

@@ -477,6 +477,7 @@ kv_read_kernel(const KvView g, const int32_t* block_table, int64_t max_pages, co
     const int64_t t = flat / g.n_heads;
     if (t >= total) return;
     while (b + 1 < n_seqs && *(cu + b + 1) <= t) ++b;
+    if (t < *(cu + b)) return;   // in front of the first sequence
     const int h = (int)(flat % g.n_heads);
     const int64_t p = (int64_t)*(first + b) + t - *(cu + b);
     int64_t page = -1;
