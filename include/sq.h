@@ -53,8 +53,8 @@ typedef enum sq_status {
                                 or size */
     SQ_ERR_CUDA = 3,         /* a CUDA runtime call failed; see sq_last_error_string() */
     SQ_ERR_TIMEOUT = 4,      /* a kernel's bounded wait ran out (reported by sq_get_status) */
-    SQ_ERR_BOUNDS = 5        /* reported by sq_get_status: a page number, length or position that a key/value
-                                cache or prompt call read on the device lies outside its range and was skipped;
+    SQ_ERR_BOUNDS = 5        /* reported by sq_get_status: a page number, length, offset or position that a key/value
+                                cache or prompt call read on the device lies outside its range and was skipped or cut;
                                 in debug builds (-DSQ_DEBUG) also a kernel's index check that found a store
                                 outside its buffer and skipped it */
 } sq_status;
@@ -515,7 +515,8 @@ typedef struct sq_kv_cache {
  *   table: as from sq_rope_table with first_pos 0, n_pos rows; NULL with
  *     rot_dim 0 for no rotation. rot_dim a multiple of 16, <= head_dim.
  *   cu_new [n_seqs + 1] int32, ascending from 0, device; rows from
- *     cu_new[n_seqs] on are neither read nor written (a padded batch).
+ *     cu_new[n_seqs] on are neither read nor written (a padded batch). Offsets outside
+ *     [0, T] or descending are cut, and sq_get_status() reports SQ_ERR_BOUNDS.
  *   ctx_len [n_seqs] int32, device: tokens the sequence holds already. The call does
  *     not change it.
  *   A page that receives tokens must belong to one sequence of the call. A
@@ -531,7 +532,8 @@ sq_status sq_rope_kv_append(const sq_kv_cache* cache, const int32_t* block_table
  *   first[b] + r - cu_out[b] of the sequence b with cu_out[b] <= r < cu_out[b+1],
  *     out = RN(code * scale), rounded once more for SQ_BF16.
  *   first [n_seqs], cu_out [n_seqs + 1] int32, ascending, device; T rows in the outputs; rows
- *   in front of cu_out[0] and from cu_out[n_seqs] on are left as they were.
+ *   in front of cu_out[0] and from cu_out[n_seqs] on are left as they were. Offsets outside
+ *   [0, T] or descending are cut, and sq_get_status() reports SQ_ERR_BOUNDS.
  *   k_out, v_out [T x n_heads x head_dim], dtype dt (SQ_F32 or SQ_BF16), contiguous. */
 sq_status sq_kv_read(const sq_kv_cache* cache, const int32_t* block_table, int64_t max_pages, const int32_t* first,
                      const int32_t* cu_out, int64_t n_seqs, int64_t T, void* k_out, void* v_out, sq_dtype dt,

@@ -540,3 +540,26 @@ def test_read_leaves_rows_before_the_first_sequence():
         got = got.cpu().numpy()
         want = np.concatenate([ref.held(codes, scales, pg.table[0], 17, 38), ref.held(codes, scales, pg.table[1], 2, 20)])
         assert np.array_equal(got[9:48], want) and np.all(got[:9] == 5.0) and np.all(got[48:] == 5.0)
+
+
+def test_append_and_read_offsets_outside_the_rows_are_cut_and_reported():
+    h, d, t = 2, 64, 100
+    ctx = [5, 17]
+    g = torch.Generator().manual_seed(8)
+    x = torch.randn((t, 2 * h, d), generator=g).to(DEV)
+    got = []
+    for cu, status in (([0, 40, 100], sq.SQ_OK), ([0, 40, 150], sq.SQ_ERR_BOUNDS), ([0, 40, 2 ** 31 - 1], sq.SQ_ERR_BOUNDS)):
+        pg = Pages([45 + 60, 17 + 60], h, d, 16, 8, seed=41)
+        _, k = sq.sq_rope_kv_append(None, x[:, :h], x[:, h:], pg.cache, pg.dev_table, ints(ctx), ints(cu), want_k=True)
+        assert sq.sq_get_status() == status and sq.sq_get_status() == sq.SQ_OK
+        kr, vr = sq.sq_kv_read(pg.cache, pg.dev_table, ints(ctx), ints(cu), t, dtype=torch.float32)
+        assert sq.sq_get_status() == status and sq.sq_get_status() == sq.SQ_OK
+        got.append((k, kr, vr, *pg.cache))
+    for other in got[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(got[0], other))
+    for cu in ([0, 60, 40], [-3, 40, 60], [0, 101, 60]):
+        pg = Pages([200, 200], h, d, 16, 8, seed=42)
+        sq.sq_rope_kv_append(None, x[:, :h], x[:, h:], pg.cache, pg.dev_table, ints(ctx), ints(cu))
+        assert sq.sq_get_status() == sq.SQ_ERR_BOUNDS
+        sq.sq_kv_read(pg.cache, pg.dev_table, ints(ctx), ints(cu), t)
+        assert sq.sq_get_status() == sq.SQ_ERR_BOUNDS

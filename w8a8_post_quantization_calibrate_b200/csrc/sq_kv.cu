@@ -98,6 +98,15 @@ __device__ __forceinline__ int warp_find(F at, int n, int64_t u) {
     return lo;
 }
 
+// By all threads of one block of a launch: offsets outside [0, rows] or descending, which the
+// kernel cuts, are reported.
+__device__ __forceinline__ void check_offsets(const int32_t* cu, int n_seqs, int64_t rows, unsigned int site) {
+    for (int b = threadIdx.x; b <= n_seqs; b += blockDim.x) {
+        const int64_t a = *(cu + b);
+        if (a < 0 || a > rows || (b > 0 && a < *(cu + b - 1))) record_status(SQ_ERR_BOUNDS, site);
+    }
+}
+
 // ---------------------------------------------------------------- 8 channels of a head
 template <typename T> struct Chunk;
 template <> struct Chunk<__nv_bfloat16> {
@@ -304,6 +313,10 @@ rope_append_kernel(const AppendArgs g) {
     const int32_t* cu = g.cu;
     const int sh = g.span_shift;
     auto start_of = [&](int b) { return (int64_t)(*(cu + b) >> sh) + 2 * (int64_t)b; };
+    if (u + 1 == gridDim.x) {   // behind the last span: a block that looks at the offsets and has nothing else in registers
+        if (blockIdx.y == 0) check_offsets(cu, g.n_seqs, g.T, SITE_KV_APPEND);
+        return;
+    }
     if (u >= start_of(g.n_seqs)) return;
     const int b = warp_find(start_of, g.n_seqs, u);
     const int64_t j = u - start_of(b);
@@ -469,6 +482,10 @@ kv_read_kernel(const KvView g, const int32_t* block_table, int64_t max_pages, co
     const int64_t id = (int64_t)blockIdx.x * 256 + threadIdx.x;
     const int64_t flat = id / LPR;
     const int c = (int)(id % LPR);
+    if (blockIdx.x + 1 == gridDim.x) {   // behind the last row
+        check_offsets(cu, n_seqs, rows, SITE_KV_READ);
+        return;
+    }
     // the block's first row by search, the thread's own from there
     const int64_t total = min(rows, (int64_t)*(cu + n_seqs));
     const int64_t t_block = (int64_t)blockIdx.x * (256 / LPR) / g.n_heads;
@@ -595,7 +612,7 @@ sq_status rope_append_impl(const sq_kv_cache* cache, const int32_t* block_table,
     g.q = q; g.k = k; g.v = v; g.q_out = q_out; g.k_out = k_out; g.table = table;
     const int span = cache->scale_block > 16 ? cache->scale_block : 16;
     g.span_shift = log2_of(span);
-    const dim3 grid((unsigned)(T / span + 2 * n_seqs), (unsigned)(2 * cache->n_heads + (n_q_heads + kQRows / span - 1) / (kQRows / span)));
+    const dim3 grid((unsigned)(T / span + 2 * n_seqs + 1), (unsigned)(2 * cache->n_heads + (n_q_heads + kQRows / span - 1) / (kQRows / span)));
     if (dt == SQ_F32) return D == 64 ? launch_append<float, 64>(g, grid, st) : launch_append<float, 128>(g, grid, st);
     return D == 64 ? launch_append<__nv_bfloat16, 64>(g, grid, st) : launch_append<__nv_bfloat16, 128>(g, grid, st);
 }
@@ -614,8 +631,8 @@ sq_status kv_read_impl(const sq_kv_cache* cache, const int32_t* block_table, int
     if (!aligned16(k_out) || !aligned16(v_out)) { set_error("outputs must be 16-byte aligned"); return SQ_ERR_UNSUPPORTED; }
     const int D = cache->head_dim;
     const int64_t blocks = (T * cache->n_heads * (D / 16) + 255) / 256;
-    if (blocks > 2147483647LL) { set_error("T too large"); return SQ_ERR_UNSUPPORTED; }
-    const dim3 grid((unsigned)blocks), block(256);
+    if (blocks >= 2147483647LL) { set_error("T too large"); return SQ_ERR_UNSUPPORTED; }
+    const dim3 grid((unsigned)blocks + 1), block(256);
 #define SQ_READ(TT, DD)                                                                                              \
     launch_pdl("kv_read_kernel", kv_read_kernel<TT, DD>, grid, block, 0, st, 1, g, block_table, max_pages, first,    \
                cu_out, (int)n_seqs, T, static_cast<TT*>(k_out), static_cast<TT*>(v_out))
