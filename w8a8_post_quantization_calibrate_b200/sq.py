@@ -641,6 +641,13 @@ def _given_or_made(t, like: torch.Tensor, shape, dtype, index: int, stream, name
     return t, _shaped(t, shape, dtype, index, name)
 
 
+def _on_device(index: int, call, *args):
+    if torch.cuda.current_device() == index:
+        return call(*args)
+    with torch.cuda.device(index):
+        return call(*args)
+
+
 def _launch(index: int, stream, name: str, *args) -> None:
     """Call a C entry point on CUDA device `index`, on `stream` or that device's
     current stream (the last C argument)."""
@@ -649,11 +656,7 @@ def _launch(index: int, stream, name: str, *args) -> None:
         st = torch._C._cuda_getCurrentRawStream(index)
     else:
         st = stream.cuda_stream if isinstance(stream, torch.cuda.Stream) else int(stream)
-    if torch.cuda.current_device() == index:
-        status = call(*args, st)
-    else:
-        with torch.cuda.device(index):
-            status = call(*args, st)
+    status = _on_device(index, call, *args, st)
     if status != SQ_OK:
         _check(status, name)
 
@@ -739,8 +742,7 @@ def sq_kv_read(cache: KvCache, block_table: torch.Tensor, first: torch.Tensor, c
 
 def sq_kv_attention_workspace_size(cache: KvCache, n_seqs: int, q_len: int, n_q_heads: int) -> int:
     c, index, _, _ = _cache_bytes(cache)
-    with torch.cuda.device(index):
-        return int(_lib.sq_kv_attention_workspace_size(c, n_seqs, q_len, n_q_heads))
+    return int(_on_device(index, _lib.sq_kv_attention_workspace_size, c, n_seqs, q_len, n_q_heads))
 
 
 def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, seq_len: torch.Tensor,
@@ -763,8 +765,7 @@ def sq_kv_attention(q: torch.Tensor, cache: KvCache, block_table: torch.Tensor, 
     if lse is not None or want_lse:
         lse, l_ptr = _given_or_made(lse, q, (n_seqs, q_len, hq), torch.float32, index, stream, "lse")
     if workspace is None:
-        # the size goes by the device's SMs, which are alike on every device of a node
-        ws_bytes = _lib.sq_kv_attention_workspace_size(c, n_seqs, q_len, hq)
+        ws_bytes = _on_device(index, _lib.sq_kv_attention_workspace_size, c, n_seqs, q_len, hq)   # by that device's SMs
         workspace, ws = _given_or_made(None, q, (ws_bytes,), torch.uint8, index, stream, "workspace")
     else:
         ws_bytes = workspace.numel()
