@@ -537,8 +537,9 @@ sq_status launch_append(const AppendArgs& g, dim3 grid, cudaStream_t st) {
     const int span = 1 << g.span_shift;
     if (span <= 2048 / D) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 128, 1>, grid, dim3(128), 0, st, 1, g);
     if (span <= RP) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 1>, grid, dim3(256), 0, st, 1, g);
-    if (span <= 2 * RP) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 2>, grid, dim3(256), 0, st, 1, g);
-    return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 4>, grid, dim3(256), 0, st, 1, g);
+    if (D == 64 || span <= 2 * RP) return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 2>, grid, dim3(256), 0, st, 1, g);
+    if constexpr (D == 128)   // a span of 128 tokens
+        return launch_pdl("rope_append_kernel", rope_append_kernel<T, D, 256, 4>, grid, dim3(256), 0, st, 1, g);
 }
 
 sq_status rope_table_impl(float* table, int64_t first, int64_t n_pos, int64_t rot, double theta,
