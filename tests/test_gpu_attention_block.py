@@ -309,3 +309,52 @@ def test_a_named_stream_inside_a_capture():
         torch.cuda.synchronize()
         assert torch.equal(a, b) and (a - 2.5).abs().max() <= 2.5 * 2.0 ** -20
     assert sq.sq_get_status() == sq.SQ_OK
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32])
+def test_the_most_sequences(dtype):
+    """65,536 sequences, most of them empty: a token here and there, one long one, all calls."""
+    n, h, hq, d, ps = 65536, 1, 4, 64, 16
+    lens = torch.zeros(n, dtype=torch.int64)
+    lens[::1000] = 1
+    lens[-1] = 300
+    lens[12345] = 77
+    cu = torch.zeros(n + 1, dtype=torch.int32)
+    cu[1:] = lens.cumsum(0)
+    t = int(cu[-1])
+    need = (lens + ps - 1) // ps
+    pages = torch.full((n, 19), -1, dtype=torch.int32)     # never read where a sequence has no token
+    order = torch.randperm(int(need.sum()), generator=torch.Generator().manual_seed(1)).int()
+    at = 0
+    for b in torch.nonzero(need).flatten().tolist():
+        pages[b, :need[b]] = order[at:at + int(need[b])]
+        at += int(need[b])
+    pages, cu, lens, zero = pages.to(DEV), cu.to(DEV), lens.int().to(DEV), torch.zeros(n, dtype=torch.int32, device=DEV)
+    g = torch.Generator().manual_seed(2)
+    x = torch.randn((t, hq + 2 * h, d), generator=g).to(dtype).to(DEV)
+    cache = sq.KvCache.empty(len(order), h, d, page_size=ps, scale_block=1)
+    q, k = sq.sq_rope_kv_append(x[:, :hq], x[:, hq:hq + h], x[:, hq + h:], cache, pages, zero, cu, want_k=True)
+    assert torch.equal(q, x[:, :hq]) and torch.equal(k, x[:, hq:hq + h])
+    kr, vr = sq.sq_kv_read(cache, pages, zero, cu, t, dtype=torch.float32)
+    step = x[:, hq:].float().abs().amax(-1, keepdim=True) / 127
+    assert ((kr - x[:, hq:hq + h].float()).abs() <= 0.5001 * step[:, :h]).all()
+    assert ((vr - x[:, hq + h:].float()).abs() <= 0.5001 * step[:, h:]).all()
+    last = torch.zeros((n, 1, hq, d), dtype=dtype, device=DEV)
+    has = lens > 0
+    last[has, 0] = q[(cu[1:][has] - 1).long()]
+    out, lse = sq.sq_kv_attention(last, cache, pages, lens, want_lse=True)
+    assert not out[~has].any() and torch.isneginf(lse[~has]).all() and torch.isfinite(lse[has]).all()
+    xb = x.bfloat16()
+    prompt = sq.sq_prompt_attention(xb[:, :hq], xb[:, hq:hq + h], xb[:, hq + h:], cu)
+    assert sq.sq_get_status() == sq.SQ_OK
+    f32 = dtype == torch.float32
+    host = [y.float().cpu().numpy() for y in (q, kr, vr, xb)]
+    out, prompt = out.float().cpu().numpy(), prompt.float().cpu().numpy()
+    for b in torch.nonzero(has).flatten().tolist():
+        a, e = int(cu[b]), int(cu[b + 1])
+        seen = np.ones((hq, e - a), bool)
+        want, _, bound, _ = ref.attention(host[0][e - 1], host[1][a:e, 0], host[2][a:e, 0], d ** -0.5, seen,
+                                          2.0 ** -22 if f32 else 2.0 ** -11, 2.0 ** -24 if f32 else 2.0 ** -8, q_step=2.0 ** -24)
+        assert np.all(np.abs(out[b, 0] - want) <= bound)
+        want, _, bound, _ = ref.attention(host[3][e - 1, :hq], host[3][a:e, hq], host[3][a:e, hq + h], d ** -0.5, seen, 2.0 ** -8, 2.0 ** -8)
+        assert np.all(np.abs(prompt[e - 1] - want) <= bound)
