@@ -49,22 +49,25 @@ struct KvAttnArgs {
 // may be any tokens: the orders here are those in which one 16-byte shared-memory
 // read gives a lane its codes without bank conflicts. S^T's accumulators become P^T's
 // operand by an 8 x 8 transpose in registers.
-//   Measured: 697 MB of a ragged batch of 64 sequences and 8 heads in 133 us, 0.80 of the
+//   Measured: 697 MB of a ragged batch of 64 sequences and 8 heads in 135 us, 0.79 of the
 // measured copy rate (its loads alone take 111); 268 MB of one sequence of 131,072
 // tokens in 51 us, 0.80. Some 40 integer and fp16
 // instructions for 16 codes keep the warps at about the pace of HBM.
 //   A code c becomes fp16 exactly: (c ^ 0x80) under the byte 0x64 is 1024 + c + 128.
 //   Scales: a key's scale multiplies its score. A value's scale multiplies its weight:
 // w = 2^(s - m) vs goes to the second product, 2^(s - m) into the sum. The reference m is
-// moved only when some |w|, or a lane's sum times 2^-80, is above 2^15 (rare after the first
+// moved only when some 2^(s - m) max(vs, 2^-80) is above 2^15 (rare after the first
 // groups); then it becomes the largest s + max(floor(log2 vs), -80), less 7, so that the
 // largest w is 2^7 .. 2^8 for scales from 2^-80 up: 2^8 below the limit, and 2^-32 of it is
 // what fp16's smallest step, 2^-24, leaves of small weights. (Kept at 1 .. 2, weights below 2^-25 of
-// the largest were lost: a sixth of a result that 32,767 of them made.)
+// the largest were lost: an eighth of a result that 32,767 of them made.)
 constexpr int kTile = 128;
 // Eight consumer warps of 224 registers, so that every accumulator and a group's codes
-// stay in them (twelve of 152 spilled: 148 us for the ragged batch of 64 sequences, eight
-// 133), and a warpgroup whose first two warps load. 168 registers at launch times 12
+// stay in them for bf16 queries, but for 160 bytes a thread with 9 to 16 rows and heads of
+// 128; fp32 queries with their second parts spill 44 to 178 bytes with heads of 128, 56
+// with 9 to 16 rows and heads of 64. (Twelve warps of 152 spilled with 8 rows too: 148 us
+// for the ragged batch of 64 sequences, eight 133 to 135.) And a warpgroup whose first two
+// warps load. 168 registers at launch times 12
 // warps are as many as 224 times 8 and 56 times 4.
 constexpr int kConsumers = 8;
 constexpr int kAttnThreads = 32 * (kConsumers + 4);
@@ -76,8 +79,10 @@ constexpr int kHeadroom = 7;                  // a new reference makes the large
 constexpr float kNoReference = -1.0e30f;      // nothing seen yet: 2^(s - m) is infinite for any score, 0 for a masked one
 // Scales below 2^-80, zero among them, count as 2^-80 where the reference is chosen and where it
 // is found too low: a weight of 2^(s - m) that its value's scale makes small or zero could
-// overflow in the sum otherwise. A lane's sum over its 4 tokens of a group stays below 2^95, that of
-// 2^30 tokens below 2^123.
+// overflow in the sum otherwise. Each stays below 2^95, the sum over 2^30 tokens below 2^125. The
+// floor costs 1% and less, but 6% with fp32 queries, heads of 64 and 128 rows (266 against 284 us
+// for 64 sequences of 4,096 tokens and 4 heads); looking at the sums, or at them only
+// where a scale is that small, cost up to 3% more with 32 to 128 rows.
 constexpr float kNoScale = -80.0f, kLeastScale = 0x1p-80f;
 
 // NB sides of 8 rows a warp, MT row tiles. MT == 1: the queries of a piece travel with its first tile.
@@ -631,9 +636,8 @@ kv_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_cons
                             const float a = exp2_fast(s[j >> 1][n][2 * (j & 1) + e] - m[n][e]);
                             sum[n][e] += a;
                             wt[j >> 1][n][2 * (j & 1) + e] = a * vs[j];
-                            most = fmaxf(most, fabsf(a * vs[j]));
+                            most = fmaxf(most, a * fmaxf(fabsf(vs[j]), kLeastScale));
                         }
-                    most = fmaxf(most, fmaxf(sum[n][0], sum[n][1]) * kLeastScale);
                 }
             };
             float most;
