@@ -300,7 +300,9 @@ constexpr int kQRows = 128;   // (position, query head) rows of one block: 8 hea
 // THREADS / (D / 16) rows cover the span. Small blocks, because a block is a chain of
 // dependent steps (its sequence, its rows, their maximum, the codes) that only
 // other blocks on the SM can hide: 1024 threads of 64 registers an SM take 62 us for five
-// prompts of 3,500 tokens and 32 heads, 512 of 126 took 81.
+// prompts of 3,500 tokens and 32 heads, 512 of 126 took 81. Each thread also reads the row
+// maxima of its whole scale block from shared memory. The four passes of a span of 128 tokens
+// and heads of 128 do not fit 64 registers and spill 624 to 660 bytes a thread.
 template <typename T, int D, int THREADS, int NP>
 __global__ void __launch_bounds__(THREADS, 1024 / THREADS)
 rope_append_kernel(const AppendArgs g) {
@@ -470,7 +472,7 @@ rope_append_kernel(const AppendArgs g) {
 
 // ================================================================== read back
 // A lane has 16 codes of K and of V of one (token, head): 16-byte loads, whole sectors both
-// ways. Bound by HBM: 870 MB of sixteen prefixes of 32 heads in 151 us, 0.88 of the
+// ways. Bound by HBM: 870 MB of sixteen prefixes of 32 heads in 153 us, 0.87 of the
 // measured copy rate.
 template <typename T, int D>
 __global__ void __launch_bounds__(256)

@@ -26,7 +26,7 @@ struct PromptArgs {
 // O += P V as tcgen05 products of 128 x 128 x D and 128 x D x 128 and about as much time
 // for the 128 x 128 exponentials of a tile as for its two products, the two query
 // tiles alternate: while one's softmax runs, the other's products do.
-//   Measured: two prompts of 5,000 and 3,185 tokens, 64 heads over 8, causal (593 GFLOP) in 622 to 647 us,
+//   Measured: two prompts of 5,000 and 3,340 tokens, 64 heads over 8, causal (593 GFLOP) in 622 to 647 us,
 // 0.92 to 0.95 PFLOP/s; 494 without the softmax. A tile's softmax takes some 1,700 cycles,
 // the other tile's two products 1,024, so the tensor cores wait for about half of the time.
 //   Tensor memory: the two tiles' scores (128 columns each, the weights in bf16 over them:
