@@ -1,5 +1,6 @@
 """Which CUDA device the attention over the cache asks for its workspace's size
-and runs on, with stand-ins for the tensors and the library (CPU only)."""
+and runs on, with stand-ins for the tensors and the library; an output without
+its input is refused (CPU only)."""
 import contextlib
 import types
 
@@ -68,3 +69,14 @@ def test_the_workspace_is_sized_on_the_caches_device(monkeypatch, current, own):
     assert calls == [(own, sizes[own])]
     assert sq.sq_kv_attention_workspace_size(cache, 3, 1, 8) == sizes[own]
     assert at == [current]
+
+
+def test_a_rotated_q_needs_a_q():
+    from w8a8_post_quantization_calibrate_b200 import build
+    build.build()
+    from w8a8_post_quantization_calibrate_b200 import sq
+    codes, scales = Standin((4, 2, 16, 64), torch.int8, 0), Standin((4, 2, 1), torch.float32, 0)
+    x = Standin((3, 2, 64), torch.bfloat16, 0)
+    with pytest.raises(ValueError, match="q_out"):
+        sq.sq_rope_kv_append(None, x, x, sq.KvCache(codes, codes, scales, scales), Standin((1, 1), torch.int32, 0),
+                             Standin((1,), torch.int32, 0), Standin((2,), torch.int32, 0), q_out=Standin((3, 4, 64), torch.bfloat16, 0))

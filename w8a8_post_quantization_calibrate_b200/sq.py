@@ -703,6 +703,8 @@ def sq_rope_kv_append(q: torch.Tensor | None, k: torch.Tensor, v: torch.Tensor, 
             raise ValueError(f"q must be [{T}, n_q_heads, {d}]")
         q_ptr, q_step = _token_rows(q, index, "q")
         q_out, qo = _given_or_made(q_out, q, (T, hq, d), dtype, index, stream, "q_out")
+    elif q_out is not None:
+        raise ValueError("q_out is given without q")
     k_ptr, k_step = _token_rows(k, index, "k")
     v_ptr, v_step = _token_rows(v, index, "v")
     ko = None
