@@ -71,10 +71,11 @@ def test_the_workspace_is_sized_on_the_caches_device(monkeypatch, current, own):
     assert at == [current]
 
 
-def test_a_rotated_q_needs_a_q():
+def test_a_rotated_q_needs_a_q(monkeypatch):
     from w8a8_post_quantization_calibrate_b200 import build
     build.build()
     from w8a8_post_quantization_calibrate_b200 import sq
+    monkeypatch.setattr(sq, "_lib", types.SimpleNamespace())   # nothing to launch
     codes, scales = Standin((4, 2, 16, 64), torch.int8, 0), Standin((4, 2, 1), torch.float32, 0)
     x = Standin((3, 2, 64), torch.bfloat16, 0)
     with pytest.raises(ValueError, match="q_out"):
